@@ -20,9 +20,10 @@ from typing import Optional
 
 import numpy as np
 
-from ._lib import (INT4, MXFP4, SVDQ_ERR_HIP, SVDQ_ERR_INVALID_ARG,  # noqa: F401
+from ._lib import (BF16, F16, INT4, MXFP4, SVDQ_ERR_HIP, SVDQ_ERR_INVALID_ARG,  # noqa: F401
                    SVDQ_ERR_SHAPE, SVDQ_ERR_UNSUPPORTED_DEVICE, SVDQ_OK,
                    EXPORTED, LIB_PATH, SvdqError, check, lib, status_string)
+from .block_ops import attention, attention_workspace_size  # noqa: F401
 
 __all__ = [
     "INT4", "MXFP4", "SvdqError", "lib", "LIB_PATH", "status_string", "merge_lora",
@@ -31,6 +32,7 @@ __all__ = [
     "unfused_linear_noalloc", "NOALLOC_SCRATCH_BYTES",
     "PackedLinear", "linear", "gemm_w4a4_lora_up_gelu", "mlp_gemm_gelu_quant", "mlp",
     "pack_w4a16", "gemm_w4a16", "mfma_ceiling",
+    "BF16", "F16", "attention", "attention_workspace_size",
 ]
 
 

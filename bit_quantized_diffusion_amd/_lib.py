@@ -21,6 +21,9 @@ SVDQ_ERR_HIP = -4
 INT4 = 0
 MXFP4 = 1
 
+BF16 = 0
+F16 = 1
+
 EXPORTED = (
     "svdq_version", "svdq_status_string", "svdq_device_check",
     "svdq_packed_sizes", "svdq_act_sizes", "svdq_pack_weights",
@@ -29,6 +32,7 @@ EXPORTED = (
     "svdq_gemm_w4a4_lora_up_gelu", "svdq_mlp_gemm_gelu_quant",
     "svdq_pack_w4a16", "svdq_gemm_w4a16", "svdq_bench_mfma_ceiling",
     "svdq_unfused_linear_noalloc", "svdq_gemm_workspace_size", "svdq_gemm_w4a4_lora_up_ws",
+    "svdq_attention_workspace_size", "svdq_attention",
 )
 
 
@@ -71,6 +75,9 @@ def _load():
         "svdq_unfused_linear_noalloc": ([vp, i, i, vp, vp, i, vp, vp, vp, vp, i, i, vp, vp], i),
         "svdq_gemm_workspace_size": ([i, i, i, i, sz], i),
         "svdq_gemm_w4a4_lora_up_ws": ([vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, ctypes.c_size_t, vp], i),
+        "svdq_attention_workspace_size": ([i, i, i, i, i, i, sz], i),
+        "svdq_attention": ([vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp, ctypes.c_float, i, i, vp, ctypes.c_size_t,
+                            vp], i),
     }
     for name, (args, ret) in sig.items():
         fn = getattr(lib, name)

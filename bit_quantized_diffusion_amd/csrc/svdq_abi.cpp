@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -44,6 +45,18 @@ int current_device_ok() {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int check_dtype(int dtype) { return dtype == SVDQ_BF16 || dtype == SVDQ_F16 ? SVDQ_OK : SVDQ_ERR_INVALID_ARG; }
+
+int check_attention_shape(int total_q, int total_k, int batch, int heads_q, int heads_k, int head_dim) {
+  if (total_q < 0 || total_k < 0 || batch < 1 || heads_q < 1 || heads_k < 1 || heads_q % heads_k) return SVDQ_ERR_SHAPE;
+  if (head_dim < 8 || head_dim > 128 || head_dim % 8) return SVDQ_ERR_SHAPE;
+  // the rows of one key head, and the workgroups (32 rows or more each, at
+  // most 64 splits), are counted in 31 bits
+  const long long rows = static_cast<long long>(total_q) * (heads_q / heads_k);
+  if (rows >= 1LL << 31 || (rows / 32 + batch) * heads_k * 64 >= 1LL << 31) return SVDQ_ERR_SHAPE;
+  return SVDQ_OK;
+}
 
 int hip_status(int e) { return e == 0 ? SVDQ_OK : SVDQ_ERR_HIP; }
 
@@ -284,6 +297,47 @@ int svdq_unfused_linear_noalloc(const void* x, int M, int K, const float* smooth
   if ((st = current_device_ok())) return st;
   return hip_status(svdq_launch_unfused_linear_noalloc(x, M, K, smooth_inv, lora_down, rank, wq, ws, lora_up, bias, N,
                                                        precision, y, stream));
+}
+
+int svdq_attention_workspace_size(int total_q, int total_k, int batch, int heads_q, int heads_k, int head_dim,
+                                  size_t* out_bytes) {
+  if (!out_bytes) return SVDQ_ERR_INVALID_ARG;
+  *out_bytes = 0;
+  const int st = check_attention_shape(total_q, total_k, batch, heads_q, heads_k, head_dim);
+  if (st) return st;
+  *out_bytes = svdq_attention_plan_bytes(total_q, total_k, batch, heads_q, heads_k, head_dim);
+  return SVDQ_OK;
+}
+
+int svdq_attention(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_seqlens_q,
+                   const int32_t* cu_seqlens_k, int batch, int total_q, int total_k, int heads_q, int heads_k,
+                   int head_dim, const int64_t* strides, float scale, int causal, int dtype, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  int st = check_dtype(dtype);
+  if (st) return st;
+  if ((st = check_attention_shape(total_q, total_k, batch, heads_q, heads_k, head_dim))) return st;
+  if (!strides || (total_q > 0 && (!q || !o)) || (total_q > 0 && total_k > 0 && (!k || !v))) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(workspace))
+    return SVDQ_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(cu_seqlens_q) |
+       reinterpret_cast<uintptr_t>(cu_seqlens_k)) & 3u)
+    return SVDQ_ERR_INVALID_ARG;
+  if (!cu_seqlens_q != !cu_seqlens_k || (!cu_seqlens_q && batch != 1)) return SVDQ_ERR_INVALID_ARG;
+  for (int i = 0; i < 8; ++i)
+    if (strides[i] < 0 || strides[i] % 8 || strides[i] > 1LL << 40) return SVDQ_ERR_INVALID_ARG;
+  int64_t own[8];
+  std::memcpy(own, strides, sizeof(own));
+  for (int i = 2; i <= 4; i += 2) {
+    // one key has no stride; rows past it must still lie outside
+    if (total_k <= 1) own[i] = head_dim;
+    if (own[i] < head_dim || own[i] > 1 << 23) return SVDQ_ERR_INVALID_ARG;
+  }
+  if (!(scale > 0.f) || std::isinf(scale)) return SVDQ_ERR_INVALID_ARG;
+  if ((st = current_device_ok())) return st;
+  if (total_q == 0) return SVDQ_OK;
+  return hip_status(svdq_launch_attention(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, batch, total_q, total_k, heads_q,
+                                          heads_k, head_dim, own, scale, causal != 0, dtype, workspace,
+                                          workspace_bytes, stream));
 }
 
 int svdq_bench_mfma_ceiling(int precision, int blocks, int iters, float* out, void* stream) {

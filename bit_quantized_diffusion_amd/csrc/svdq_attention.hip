@@ -1,0 +1,675 @@
+// Attention over packed sequences for gfx950.
+//
+//   s_ij = scale q_i . k_j,  p_ij = exp(s_ij - lse_i),  o_i = sum_j p_ij v_j,
+//   lse_i = log sum_j exp(s_ij)
+//
+// over the keys j of the query's own sequence, with causal masking counted
+// from the sequences' ends: query i of len_q sees key j of len_k iff
+// j <= i + len_k - len_q.  A query with no key gives o = 0, lse = -inf.
+//
+// Rows.  The g = heads_q / heads_k query heads that share a key head are
+// packed with their tokens into one axis of len_q g rows (row R: token R / g,
+// head R % g of the group), so that a tile of rows reads each key once for
+// all of them and a single token still fills g rows.
+//
+// Products.  A wave owns 32 rows.  It computes S^T = K Q^T, so that a lane
+// holds scores of one row only (column l % 32 of the result): the row's
+// maximum and sum are in-lane operations plus one exchange with the lane 32
+// away.  The result's registers are, rounded to 16 bits, already the B
+// operand of O^T = V^T P^T if the sum over keys runs in the order in which
+// they lie there: keys 16 k + 4 h + {0..3, 8..11} for lane half h.  The V^T
+// operand is read in that order by two transposing LDS reads (4 keys each).
+//
+// Softmax.  One pass: running reference m, sum l and O are rescaled only
+// when a row's maximum exceeds m by more than 2^8 in the exponent's base
+// (exact for any m, since o = O / l and P <= 256 keeps its relative
+// precision); O and l are held in fp32, P is rounded to 16 bits to nearest
+// even for the matrix core and l sums the unrounded values.
+
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "svdq_device.h"
+#include "svdq_internal.h"
+
+namespace {
+
+using namespace svdq_dev;
+
+struct AttnArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t* o;
+  float* lse;            // [total_q][heads_q] or null
+  float* part_o;         // [splits][total_q][heads_q][D], splits > 1
+  float2* part_ml;       // [splits][total_q][heads_q] {m, l}
+  const int32_t *cu_q, *cu_k;   // null: one sequence
+  int64_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h;   // strides in elements
+  int total_q, total_k, batch, heads_q, heads_k, group, D;
+  float scale;           // > 0
+  int causal, splits, slots;
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.f;   // log2 of the largest P before a rescale
+
+struct Tile {
+  int q0, len_q, k0, len_k;   // the sequence's tokens
+  int row0, rows;             // first row of the tile, rows of the sequence
+  bool any;
+};
+
+// Rows are cut into tiles of BM per sequence.  Sequence i owns the slots
+// from floor(cu[i] g / BM) + i up to the next sequence's first: at least as
+// many as it has tiles, and known without reading lengths on the host.  The
+// slots left over exit.  The owner of a slot is found by a 64-way search.
+template <int BM>
+__device__ __forceinline__ Tile find_tile(const AttnArgs& a, int slot) {
+  int seq = 0;
+  if (a.batch > 1) {
+    const int lane = threadIdx.x & 63;
+    int n = a.batch;
+    while (n > 1) {
+      const int step = (n + 63) >> 6;
+      const int i = seq + lane * step;
+      bool before = false;
+      if (lane * step < n) {
+        const int64_t rows = static_cast<int64_t>(min(max(a.cu_q[i], 0), a.total_q)) * a.group;
+        before = rows / BM + i <= slot;
+      }
+      const int c = max(static_cast<int>(__popcll(__ballot(before))), 1);
+      const int next = seq + (c - 1) * step;
+      n = min(step, n - (c - 1) * step);
+      seq = next;
+    }
+    seq = __builtin_amdgcn_readfirstlane(seq);
+  }
+  Tile t;
+  t.q0 = 0;
+  t.len_q = a.total_q;
+  int64_t first = 0;
+  if (a.cu_q) {
+    t.q0 = min(max(a.cu_q[seq], 0), a.total_q);
+    t.len_q = min(max(a.cu_q[seq + 1], t.q0), a.total_q) - t.q0;
+    first = static_cast<int64_t>(t.q0) * a.group / BM + seq;
+  }
+  t.k0 = 0;
+  t.len_k = a.total_k;
+  if (a.cu_k) {
+    t.k0 = min(max(a.cu_k[seq], 0), a.total_k);
+    t.len_k = min(max(a.cu_k[seq + 1], t.k0), a.total_k) - t.k0;
+  }
+  t.rows = t.len_q * a.group;
+  const int64_t row0 = (slot - first) * BM;
+  t.any = slot >= first && row0 < t.rows;
+  t.row0 = t.any ? static_cast<int>(row0) : 0;
+  return t;
+}
+
+// One K or V tile of KEYS keys in LDS: rows of DP 16-bit values, unpadded.
+// The 16-byte chunk c of row r sits at chunk c ^ f(r):
+//   K  read 16 bytes a lane from 32 consecutive rows at one chunk: f takes
+//      all values over the rows whose chunks share a 256-byte LDS line set;
+//   V  read transposed, 64-byte segments of 4 consecutive rows: f moves the
+//      4 rows' segments into distinct quarters of a line.
+template <int DP>
+__device__ __forceinline__ int swz_k(int r) { return DP == 128 ? (r & 15) : ((r >> 1) & 7); }
+template <int DP>
+__device__ __forceinline__ int swz_v(int r) { return DP == 128 ? (r & 3) << 2 : (r & 2) << 1; }
+
+// byte offset in memory (from the tile's first row) of the chunk that lane
+// `lane` of load `n` of a tile brings in; chunks past D lie outside
+template <int DP, bool ISV>
+__device__ __forceinline__ int tile_voff(int n, int lane, int64_t stride, int D) {
+  constexpr int kChunks = DP / 8;
+  const int r = n * (64 / kChunks) + lane / kChunks;
+  const int c = (lane % kChunks) ^ (ISV ? swz_v<DP>(r) : swz_k<DP>(r));
+  return c * 8 < D ? static_cast<int>(r * stride * 2) + c * 16 : kOutside;
+}
+
+template <typename E, int DP, int KEYS>
+struct WaveTile {
+  static constexpr int kKt = KEYS / 32;        // 32-key tiles of S^T
+  static constexpr int kDt = DP / 32;          // 32-wide tiles of O^T
+  static constexpr int kSteps = DP / 16;       // k steps of the first product
+  static constexpr int kBytes = KEYS * DP * 2;
+
+  v4u qf[kSteps];
+  v16f acc[kDt];
+  float m, l, msc, limit;   // reference, sum, m scale log2(e), m + slack
+  float sc, slack;          // scale log2(e), slack in score units
+  uint32_t ka[kSteps], va[kDt];   // LDS offsets of the lane's reads
+
+  __device__ __forceinline__ void init(const AttnArgs& a, int lane) {
+    const int l32 = lane & 31, h = lane >> 5, i16 = lane & 15;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) ka[s] = l32 * DP * 2 + (((2 * s + h) ^ swz_k<DP>(l32)) << 4);
+    const int vr = 4 * h + (i16 >> 2);           // row within 8 keys
+#pragma unroll
+    for (int d = 0; d < kDt; ++d) {
+      const int c = d * 4 + ((lane >> 4) & 1) * 2 + ((i16 & 3) >> 1);
+      va[d] = vr * DP * 2 + ((c ^ swz_v<DP>(vr)) << 4) + (i16 & 1) * 8;
+    }
+#pragma unroll
+    for (int d = 0; d < kDt; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
+    sc = a.scale * kLog2e;
+    slack = kSlack / sc;
+    m = limit = -INFINITY;
+    l = msc = 0.f;
+  }
+
+  // Q fragment: lane (row l % 32, half h), step s: d = 16 s + 8 h .. + 7
+  __device__ __forceinline__ void load_q(const uint16_t* row, bool valid, int h, int D) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      qf[s] = v4u{0, 0, 0, 0};
+      if (valid && 16 * s + 8 * h < D) qf[s] = *reinterpret_cast<const v4u*>(row + 16 * s + 8 * h);
+    }
+  }
+
+  __device__ __forceinline__ void scores(uint32_t kbuf, v16f (&s)[kKt]) const {
+#pragma unroll
+    for (int kt = 0; kt < kKt; ++kt)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[kt][e] = 0.f;
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+      for (int kt = 0; kt < kKt; ++kt) s[kt] = E::mfma(lds_read16(kbuf + ka[st] + kt * 32 * DP * 2), qf[st], s[kt]);
+  }
+
+  // keys key0 + .. at or past lim are out of the row's sight
+  __device__ __forceinline__ void mask(v16f (&s)[kKt], int key0, int lim, int h) const {
+    const int left = lim - key0 - 4 * h;
+#pragma unroll
+    for (int kt = 0; kt < kKt; ++kt)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[kt][e] = kt * 32 + (e >> 2) * 8 + (e & 3) < left ? s[kt][e] : -INFINITY;
+  }
+
+  // the row's maximum against the reference; O and l move to a new
+  // reference if any row of the wave needs it
+  __device__ __forceinline__ void raise(const v16f (&s)[kKt]) {
+    float mx = s[0][0];
+#pragma unroll
+    for (int kt = 0; kt < kKt; ++kt)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mx = __builtin_elementwise_maximum(mx, s[kt][e]);
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
+    mx = __builtin_elementwise_maximum(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    if (__ballot(mx > limit)) {
+      const float m_new = mx > m ? mx : m;
+      const float f = m == -INFINITY ? 0.f : exp2_fast((m - m_new) * sc);
+#pragma unroll
+      for (int d = 0; d < kDt; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[d][e] *= f;
+      l *= f;
+      m = m_new;
+      limit = m + slack;
+      msc = m == -INFINITY ? 0.f : m * sc;
+    }
+  }
+
+  __device__ __forceinline__ void weights(v16f (&s)[kKt], v4u (&p)[2 * kKt]) {
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kt = 0; kt < kKt; ++kt)
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float a = exp2_fast(__builtin_fmaf(s[kt][e], sc, -msc));
+        const float b = exp2_fast(__builtin_fmaf(s[kt][e + 1], sc, -msc));
+        part[(e >> 1) & 1] += a;
+        part[2 + ((e >> 1) & 1)] += b;
+        p[2 * kt + (e >> 3)][(e >> 1) & 3] = E::pack2(a, b);
+      }
+    l += (part[0] + part[1]) + (part[2] + part[3]);
+  }
+
+  __device__ __forceinline__ void accumulate(uint32_t vbuf, const v4u (&p)[2 * kKt]) {
+#pragma unroll
+    for (int ks = 0; ks < 2 * kKt; ++ks)
+#pragma unroll
+      for (int d = 0; d < kDt; ++d) {
+        const v2u lo = lds_read_tr(vbuf + va[d] + ks * 16 * DP * 2);
+        const v2u hi = lds_read_tr(vbuf + va[d] + (ks * 16 + 8) * DP * 2);
+        acc[d] = E::mfma(v4u{lo.x, lo.y, hi.x, hi.y}, p[ks], acc[d]);
+      }
+  }
+
+  // the two halves of a row hold the sums of different keys
+  __device__ __forceinline__ float row_sum() const {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+};
+
+__device__ __forceinline__ float lse_of(float m, float l, float scale) { return l == 0.f ? -INFINITY : m * scale + logf(l); }
+
+// Workgroup -> (slot, key head, split).  The workgroups of one (head, split)
+// read the same keys; where the units divide evenly, each of the 8 XCDs
+// (consecutive ids go to consecutive XCDs) takes whole units, so that its L2
+// holds them.  Causal tiles run longest first.
+struct Job {
+  int slot, head, split;
+};
+__device__ __forceinline__ Job job_of(const AttnArgs& a, int id) {
+  const int units = a.heads_k * a.splits;
+  int w = id;
+  if ((units & 7) == 0) w = (id & 7) * (units >> 3) * a.slots + (id >> 3);
+  const int unit = w / a.slots;
+  const int slot = w - unit * a.slots;
+  Job j;
+  j.slot = a.causal ? a.slots - 1 - slot : slot;
+  j.head = unit / a.splits;
+  j.split = unit - j.head * a.splits;
+  return j;
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: NW waves of 32 rows share tiles of 64 keys.
+//
+// K runs one tile ahead of V: iteration i multiplies Q with K tile i + 1
+// while the softmax of tile i runs on the vector units, so that matrix and
+// vector work of one wave overlap, and two waves share a SIMD.  Tiles come
+// straight to LDS, double-buffered, with one barrier an iteration.
+// ---------------------------------------------------------------------------
+
+template <typename E, int DP, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
+  constexpr int kKeys = 64, BM = NW * 32;
+  using W = WaveTile<E, DP, kKeys>;
+  constexpr int kBuf = W::kBytes;
+  constexpr int kLoads = kBuf / 1024 / NW;   // 1 KB loads per wave and operand tile
+  static_assert(kLoads >= 1 && NW * 32 * DP * 2 <= 4 * kBuf, "loads divide evenly; the output staging fits");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBuf];   // K0 K1 V0 V1
+
+  const Job job = job_of(a, blockIdx.x);
+  const Tile t = find_tile<BM>(a, job.slot);
+  if (!t.any) return;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // this lane's row
+  const int row = t.row0 + wave * 32 + l32;
+  const bool valid = row < t.rows;
+  const int token = row / a.group;
+  const int head = job.head * a.group + (row - token * a.group);
+  const int shift = t.len_k - t.len_q + 1;
+  const int lim = !valid ? 0x7FFFFFFF : a.causal ? token + shift : t.len_k;
+
+  W w;
+  w.init(a, lane);
+  w.load_q(a.q + (t.q0 + token) * a.q_t + head * a.q_h, valid, h, a.D);
+
+  // key tiles: up to the last row's limit; the first `open` need no mask
+  const int last_row = min(t.row0 + BM, t.rows) - 1;
+  const int end = a.causal ? min(t.len_k, last_row / a.group + shift) : t.len_k;
+  const int tiles = (max(end, 0) + kKeys - 1) / kKeys;
+  const int first_lim = a.causal ? min(t.len_k, t.row0 / a.group + shift) : t.len_k;
+  const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * job.split / a.splits);
+  const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (job.split + 1) / a.splits);
+  const int open = min(max(first_lim, 0) / kKeys, t1);
+
+  int kv[kLoads], vv[kLoads];
+#pragma unroll
+  for (int n = 0; n < kLoads; ++n) {
+    kv[n] = tile_voff<DP, false>(wave * kLoads + n, lane, a.k_t, a.D);
+    vv[n] = tile_voff<DP, true>(wave * kLoads + n, lane, a.v_t, a.D);
+  }
+  const uint32_t base = lds_addr(lds);
+  const uint32_t dst = base + wave * kLoads * 1024;
+  const uint16_t* const kp = a.k + t.k0 * a.k_t + job.head * a.k_h;
+  const uint16_t* const vp = a.v + t.k0 * a.v_t + job.head * a.v_h;
+  auto load_k = [&](int i, int buf) {
+    const int left = t.len_k - i * kKeys;
+    const auto r = buffer_of(kp + i * kKeys * a.k_t, (left - 1) * a.k_t * 2 + a.D * 2);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) dma_b128(r, dst + buf * kBuf + n * 1024, kv[n]);
+  };
+  auto load_v = [&](int i, int buf) {
+    const int left = t.len_k - i * kKeys;
+    const auto r = buffer_of(vp + i * kKeys * a.v_t, (left - 1) * a.v_t * 2 + a.D * 2);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) dma_b128(r, dst + (2 + buf) * kBuf + n * 1024, vv[n]);
+  };
+
+  v16f s[W::kKt];
+  if (t0 < t1) {
+    load_k(t0, 0);
+    load_v(t0, 0);
+    if (t0 + 1 < t1) load_k(t0 + 1, 1);
+    lds_wait_barrier<0>();
+    w.scores(base, s);
+    lds_wait_barrier<0>();
+
+    auto iterate = [&](int i, auto masked, auto next) {
+      const int b = (i - t0) & 1;
+      if (i + 2 < t1) load_k(i + 2, b);
+      if (i + 1 < t1) load_v(i + 1, b ^ 1);
+      if constexpr (decltype(masked)::value) w.mask(s, i * kKeys, lim, h);
+      w.raise(s);
+      v4u p[2 * W::kKt];
+      v16f s_next[W::kKt];
+      if constexpr (decltype(next)::value) w.scores(base + (b ^ 1) * kBuf, s_next);
+      w.weights(s, p);
+      w.accumulate(base + (2 + b) * kBuf, p);
+      lds_wait_barrier<0>();
+      if constexpr (decltype(next)::value) {
+#pragma unroll
+        for (int kt = 0; kt < W::kKt; ++kt) s[kt] = s_next[kt];
+      }
+    };
+    int i = t0;
+    for (; i < min(open, t1 - 1); ++i) iterate(i, std::false_type{}, std::true_type{});
+    for (; i < t1 - 1; ++i) iterate(i, std::true_type{}, std::true_type{});
+    iterate(i, std::true_type{}, std::false_type{});
+  }
+
+  const float l = w.row_sum();
+  const int64_t out_row = static_cast<int64_t>(t.q0 + token) * a.heads_q + head;
+  if (a.splits > 1) {
+    if (valid) {
+      const int64_t part = static_cast<int64_t>(job.split) * a.total_q * a.heads_q + out_row;
+      if (h == 0) a.part_ml[part] = make_float2(w.m, l);
+      float* po = a.part_o + part * a.D;
+#pragma unroll
+      for (int d = 0; d < W::kDt; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (d * 32 + 8 * j + 4 * h < a.D)
+            *reinterpret_cast<v4f*>(po + d * 32 + 8 * j + 4 * h) =
+                v4f{w.acc[d][4 * j], w.acc[d][4 * j + 1], w.acc[d][4 * j + 2], w.acc[d][4 * j + 3]};
+    }
+    return;
+  }
+  if (a.lse && valid && h == 0) a.lse[out_row] = lse_of(w.m, l, a.scale);
+  // O through the wave's own part of LDS, so that a store covers whole rows
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  constexpr int kChunks = DP / 8;
+  uint8_t* const stage = lds + wave * 32 * DP * 2;
+#pragma unroll
+  for (int d = 0; d < W::kDt; ++d)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = (d * 4 + j) ^ swz_k<DP>(l32);
+      *reinterpret_cast<v2u*>(stage + l32 * DP * 2 + c * 16 + h * 8) =
+          v2u{E::pack2(w.acc[d][4 * j] * inv, w.acc[d][4 * j + 1] * inv),
+              E::pack2(w.acc[d][4 * j + 2] * inv, w.acc[d][4 * j + 3] * inv)};
+    }
+#pragma unroll
+  for (int it = 0; it < DP / 16; ++it) {
+    const int r = it * (64 / kChunks) + lane / kChunks, c = lane % kChunks;
+    const int rr = t.row0 + wave * 32 + r;
+    const int tok = rr / a.group;
+    const v4u x = *reinterpret_cast<const v4u*>(stage + r * DP * 2 + ((c ^ swz_k<DP>(r)) << 4));
+    if (rr < t.rows && c * 8 < a.D)
+      *reinterpret_cast<v4u*>(a.o + (t.q0 + tok) * a.o_t + (job.head * a.group + rr - tok * a.group) * a.o_h + c * 8) = x;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (single tokens): 32 rows a workgroup, whose 4 waves take the key
+// tiles in turn, 32 keys each, through LDS of their own (no barrier in the
+// loop), and join their results at the end.  Bound by reading K and V.
+// ---------------------------------------------------------------------------
+
+template <typename E, int DP>
+__global__ __launch_bounds__(256, 1) void k_attention_few(AttnArgs a) {
+  constexpr int kKeys = 32, BM = 32, NW = 4;
+  using W = WaveTile<E, DP, kKeys>;
+  constexpr int kBuf = W::kBytes;          // one operand tile
+  constexpr int kLoads = kBuf / 1024;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NW * 4 * kBuf];   // per wave: K0 V0 K1 V1
+  __shared__ float lds_m[NW][32], lds_l[NW][32];
+  static_assert(32 * DP * 4 <= 4 * kBuf, "a wave's O fits in its buffers");
+
+  const Job job = job_of(a, blockIdx.x);
+  const Tile t = find_tile<BM>(a, job.slot);
+  if (!t.any) return;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  const int row = t.row0 + l32;
+  const bool valid = row < t.rows;
+  const int token = row / a.group;
+  const int head = job.head * a.group + (row - token * a.group);
+  const int shift = t.len_k - t.len_q + 1;
+  const int lim = !valid ? 0x7FFFFFFF : a.causal ? token + shift : t.len_k;
+
+  W w;
+  w.init(a, lane);
+  w.load_q(a.q + (t.q0 + token) * a.q_t + head * a.q_h, valid, h, a.D);
+
+  const int last_row = min(t.row0 + BM, t.rows) - 1;
+  const int end = a.causal ? min(t.len_k, last_row / a.group + shift) : t.len_k;
+  const int tiles = (max(end, 0) + kKeys - 1) / kKeys;
+  const int first_lim = a.causal ? min(t.len_k, t.row0 / a.group + shift) : t.len_k;
+  const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * job.split / a.splits);
+  const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (job.split + 1) / a.splits);
+
+  int kv[kLoads], vv[kLoads];
+#pragma unroll
+  for (int n = 0; n < kLoads; ++n) {
+    kv[n] = tile_voff<DP, false>(n, lane, a.k_t, a.D);
+    vv[n] = tile_voff<DP, true>(n, lane, a.v_t, a.D);
+  }
+  const uint32_t base = lds_addr(lds) + wave * 4 * kBuf;
+  const uint16_t* const kp = a.k + t.k0 * a.k_t + job.head * a.k_h;
+  const uint16_t* const vp = a.v + t.k0 * a.v_t + job.head * a.v_h;
+  auto load = [&](int i, int buf) {
+    const int left = t.len_k - i * kKeys;
+    const auto rk = buffer_of(kp + i * kKeys * a.k_t, (left - 1) * a.k_t * 2 + a.D * 2);
+    const auto rv = buffer_of(vp + i * kKeys * a.v_t, (left - 1) * a.v_t * 2 + a.D * 2);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) dma_b128(rk, base + 2 * buf * kBuf + n * 1024, kv[n]);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) dma_b128(rv, base + (2 * buf + 1) * kBuf + n * 1024, vv[n]);
+  };
+  if (t0 + wave < t1) load(t0 + wave, 0);
+  if (t0 + wave + NW < t1) load(t0 + wave + NW, 1);
+  int b = 0;
+  for (int i = t0 + wave; i < t1; i += NW, b ^= 1) {
+    if (i + NW < t1)
+      vm_wait<2 * kLoads>();   // tile i is there, tile i + NW may fly
+    else
+      vm_wait<0>();
+    v16f s[1];
+    w.scores(base + 2 * b * kBuf, s);
+    if ((i + 1) * kKeys > first_lim) w.mask(s, i * kKeys, lim, h);
+    w.raise(s);
+    v4u p[2];
+    w.weights(s, p);
+    w.accumulate(base + (2 * b + 1) * kBuf, p);
+    // the reads of this buffer are done before it is loaded again
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (i + 2 * NW < t1) load(i + 2 * NW, b);
+  }
+
+  // join the waves: common reference, then the sum of the scaled parts
+  float l = w.row_sum();
+  if (h == 0) {
+    lds_m[wave][l32] = w.m;
+    lds_l[wave][l32] = l;
+  }
+  __syncthreads();
+  float m_all = lds_m[0][l32];
+#pragma unroll
+  for (int i = 1; i < NW; ++i) m_all = lds_m[i][l32] > m_all ? lds_m[i][l32] : m_all;
+  const float f = w.m == -INFINITY ? 0.f : exp2_fast((w.m - m_all) * w.sc);
+  constexpr int kRow = DP + 4;   // floats; the pad spreads rows over banks
+  float* const mine = reinterpret_cast<float*>(lds + wave * 4 * kBuf);
+  static_assert(32 * kRow * 4 <= 4 * kBuf, "a wave's O fits in its buffers");
+#pragma unroll
+  for (int d = 0; d < W::kDt; ++d)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<v4f*>(mine + l32 * kRow + d * 32 + 8 * j + 4 * h) =
+          v4f{w.acc[d][4 * j] * f, w.acc[d][4 * j + 1] * f, w.acc[d][4 * j + 2] * f, w.acc[d][4 * j + 3] * f};
+  if (h == 0) lds_l[wave][l32] = l * f;
+  __syncthreads();
+  // thread: row threadIdx.x / 8, every eighth 4 columns
+  const int r = threadIdx.x >> 3;
+  const int rr = t.row0 + r;
+  if (rr >= t.rows) return;
+  float m_row = lds_m[0][r], l_row = lds_l[0][r];
+#pragma unroll
+  for (int i = 1; i < NW; ++i) {
+    m_row = lds_m[i][r] > m_row ? lds_m[i][r] : m_row;
+    l_row += lds_l[i][r];
+  }
+  const int tok = rr / a.group;
+  const int hd = job.head * a.group + rr - tok * a.group;
+  const int64_t out_row = static_cast<int64_t>(t.q0 + tok) * a.heads_q + hd;
+  const int64_t part = static_cast<int64_t>(job.split) * a.total_q * a.heads_q + out_row;
+  const bool whole = a.splits == 1;
+  if ((threadIdx.x & 7) == 0) {
+    if (!whole)
+      a.part_ml[part] = make_float2(m_row, l_row);
+    else if (a.lse)
+      a.lse[out_row] = lse_of(m_row, l_row, a.scale);
+  }
+  const float inv = l_row == 0.f ? 0.f : 1.f / l_row;
+  for (int d = (threadIdx.x & 7) * 4; d < a.D; d += 32) {
+    v4f x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NW; ++i) x += *reinterpret_cast<const v4f*>(reinterpret_cast<float*>(lds + i * 4 * kBuf) + r * kRow + d);
+    if (whole)
+      *reinterpret_cast<v2u*>(a.o + (t.q0 + tok) * a.o_t + hd * a.o_h + d) =
+          v2u{E::pack2(x[0] * inv, x[1] * inv), E::pack2(x[2] * inv, x[3] * inv)};
+    else
+      *reinterpret_cast<v4f*>(a.part_o + part * a.D + d) = x;
+  }
+}
+
+// Join of the splits: a wave per row, in the order of the splits.  A split
+// that saw no key wrote l = 0 and is left out (its O is not read).
+template <typename E>
+__global__ __launch_bounds__(256) void k_attention_join(AttnArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t rows = static_cast<int64_t>(a.total_q) * a.heads_q;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (row >= rows) return;
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (lane < a.splits) ml = a.part_ml[lane * rows + row];
+  float m = ml.x;
+#pragma unroll
+  for (int o = 32; o; o >>= 1) {
+    const float x = __shfl_xor(m, o);
+    m = x > m ? x : m;
+  }
+  const float f = ml.y == 0.f ? 0.f : exp2_fast((ml.x - m) * (a.scale * kLog2e));
+  float l = ml.y * f;
+#pragma unroll
+  for (int o = 32; o; o >>= 1) l += __shfl_xor(l, o);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  float x0 = 0.f, x1 = 0.f;
+  const int d = 2 * lane;
+  for (int s = 0; s < a.splits; ++s) {
+    const float fs = __shfl(f, s);
+    if (__shfl(ml.y, s) != 0.f && d < a.D) {
+      const float2 x = *reinterpret_cast<const float2*>(a.part_o + (s * rows + row) * a.D + d);
+      x0 += x.x * fs;
+      x1 += x.y * fs;
+    }
+  }
+  const int64_t tok = row / a.heads_q;
+  if (d < a.D)
+    *reinterpret_cast<uint32_t*>(a.o + tok * a.o_t + (row - tok * a.heads_q) * a.o_h + d) = E::pack2(x0 * inv, x1 * inv);
+  if (a.lse && lane == 0) a.lse[row] = lse_of(m, l, a.scale);
+}
+
+struct Plan {
+  int waves;     // rows a workgroup takes / 32; 0: k_attention_few
+  int splits;
+  size_t bytes;
+};
+
+// The schedule from the sizes the host knows.  Lengths are on the device, so
+// the mean stands for them; every schedule is right for any lengths.
+Plan plan_for(int total_q, int total_k, int batch, int heads_q, int heads_k, int D) {
+  const int64_t rows = static_cast<int64_t>(total_q) * (heads_q / heads_k);
+  const int64_t mean_rows = rows / batch, mean_keys = total_k / batch;
+  Plan p;
+  p.waves = mean_rows <= 64 ? 0 : 8;
+  const int bm = p.waves ? p.waves * 32 : 32;
+  const int64_t units = (rows / bm > batch ? rows / bm : batch) * heads_k;
+  const int64_t want = p.waves ? 256 : 1024, keys = p.waves ? 512 : 256;
+  int64_t s = units >= want / 2 ? 1 : (want + units - 1) / units;
+  if (s > mean_keys / keys) s = mean_keys / keys;
+  p.splits = static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
+  p.bytes = p.splits == 1 ? 0 : static_cast<size_t>(p.splits) * total_q * heads_q * (D + 2) * 4;
+  return p;
+}
+
+template <typename E>
+int launch(AttnArgs a, const Plan& p, hipStream_t stream) {
+  const int bm = p.waves ? p.waves * 32 : 32;
+  a.splits = p.splits;
+  a.slots = static_cast<int>(static_cast<int64_t>(a.total_q) * a.group / bm) + a.batch;
+  const dim3 grid(static_cast<unsigned>(a.slots) * a.heads_k * a.splits);
+  const bool wide = a.D > 64;
+  if (p.waves == 8) {
+    if (wide)
+      k_attention<E, 128, 8><<<grid, 512, 0, stream>>>(a);
+    else
+      k_attention<E, 64, 8><<<grid, 512, 0, stream>>>(a);
+  } else {
+    if (wide)
+      k_attention_few<E, 128><<<grid, 256, 0, stream>>>(a);
+    else
+      k_attention_few<E, 64><<<grid, 256, 0, stream>>>(a);
+  }
+  if (a.splits > 1) {
+    const int64_t rows = static_cast<int64_t>(a.total_q) * a.heads_q;
+    k_attention_join<E><<<dim3(static_cast<unsigned>((rows + 3) / 4)), 256, 0, stream>>>(a);
+  }
+  return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t svdq_attention_plan_bytes(int total_q, int total_k, int batch, int heads_q, int heads_k, int head_dim) {
+  return plan_for(total_q, total_k, batch, heads_q, heads_k, head_dim).bytes;
+}
+
+int svdq_launch_attention(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_q,
+                          const int32_t* cu_k, int batch, int total_q, int total_k, int heads_q, int heads_k,
+                          int head_dim, const int64_t* strides, float scale, int causal, int dtype, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  Plan p = plan_for(total_q, total_k, batch, heads_q, heads_k, head_dim);
+  if (!workspace || workspace_bytes < p.bytes) p.splits = 1;
+  AttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.o = static_cast<uint16_t*>(o);
+  a.lse = lse;
+  if (p.splits > 1) {
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(p.splits) * total_q * heads_q * head_dim);
+  }
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.q_t = strides[0], a.q_h = strides[1], a.k_t = strides[2], a.k_h = strides[3];
+  a.v_t = strides[4], a.v_h = strides[5], a.o_t = strides[6], a.o_h = strides[7];
+  a.total_q = total_q;
+  a.total_k = total_k;
+  a.batch = batch;
+  a.heads_q = heads_q;
+  a.heads_k = heads_k;
+  a.group = heads_q / heads_k;
+  a.D = head_dim;
+  a.scale = scale;
+  a.causal = causal;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  return dtype == SVDQ_BF16 ? launch<Bf16>(a, p, s) : launch<F16>(a, p, s);
+}
+
+}  // extern "C"

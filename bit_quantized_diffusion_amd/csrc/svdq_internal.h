@@ -79,6 +79,12 @@ int svdq_launch_unfused_linear(const void* x, int M, int K,
                                const void* lora_up, const void* bias, int N,
                                int precision, uint8_t* xq, void* xs,
                                float* lora_act, void* y, void* stream);
+// Workspace bytes of svdq_launch_attention for these sizes (0: no split).
+size_t svdq_attention_plan_bytes(int total_q, int total_k, int batch, int heads_q, int heads_k, int head_dim);
+int svdq_launch_attention(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_q,
+                          const int32_t* cu_k, int batch, int total_q, int total_k, int heads_q, int heads_k,
+                          int head_dim, const int64_t* strides, float scale, int causal, int dtype, void* workspace,
+                          size_t workspace_bytes, void* stream);
 int svdq_launch_mfma_ceiling(int precision, int blocks, int iters, float* out, void* stream);
 int svdq_launch_unfused_linear_noalloc(const void* x, int M, int K, const float* smooth_inv, const void* lora_down,
                                        int rank, const uint8_t* wq, const void* ws, const void* lora_up,

@@ -318,6 +318,55 @@ SVDQ_API int svdq_unfused_linear_noalloc(const void* x, int M, int K,
                         const void* lora_up, const void* bias, int N, int precision,
                         void* y, void* stream);
 
+/* ---------------------------------------------------------------------
+ * 16-bit operators that stand between the quantized linears of a
+ * transformer block.  Values are bf16 or fp16 (dtype), held in fp32 between
+ * load and the one rounding to nearest even at the end.  They allocate
+ * nothing; conventions, errors and streams are those of the hot calls.
+ * --------------------------------------------------------------------- */
+#define SVDQ_BF16  0
+#define SVDQ_F16   1
+
+/* Attention over packed sequences with grouped heads.
+ *
+ *   s_ij = scale q_i . k_j over the keys j of query i's sequence,
+ *   o_i = sum_j softmax_j(s_ij) v_j,   lse_i = log sum_j exp(s_ij)
+ *
+ *   q, o   (dev) [total_q][heads_q][head_dim]   token and head strides below
+ *   k, v   (dev) [total_k][heads_k][head_dim]
+ *   lse    (dev) [total_q][heads_q] fp32, out, or NULL
+ *   cu_seqlens_q, cu_seqlens_k (dev) [batch+1] int32 each: sequence b holds
+ *          queries cu_q[b] .. cu_q[b+1]-1 and keys cu_k[b] .. cu_k[b+1]-1.
+ *          They start at 0, do not fall and end at total_q and total_k;
+ *          sequences may be empty on either side.  Values outside that are
+ *          cut to [0, total], so no access leaves the tensors.  NULL (both,
+ *          batch == 1): one sequence of all tokens.
+ *   strides (host) 8 strides in elements: q token, q head, k token, k head,
+ *          v token, v head, o token, o head.  Multiples of 8, not negative;
+ *          k and v token strides in [head_dim, 2^23] when total_k > 1.  The last dimension
+ *          is dense.  Q, K and V can so be read out of one fused projection.
+ * Query head h reads key head h / (heads_q / heads_k).
+ * causal != 0: counted from the sequences' ends, query i sees keys
+ * j <= i + len_k - len_q (the last query sees the last key; with one query
+ * all keys).  A query that sees no key gives o = 0 and lse = -inf.  Keys
+ * that no query of a row's sequence can see, and what lies past a
+ * sequence's end, may hold anything; a NaN or infinity in v at a key hidden
+ * from a query only by the causal rule can reach that query's o (0 * NaN).
+ * head_dim: a multiple of 8, 8 to 128.  total_q, total_k >= 0,
+ * total_q (heads_q / heads_k) < 2^31.  scale > 0 and finite.
+ * workspace (dev, 16-byte aligned): with the bytes that
+ * svdq_attention_workspace_size names, calls with few queries (single
+ * tokens against long caches) cut each sequence's keys into parts whose
+ * results a second kernel joins in a fixed order; with NULL or fewer bytes
+ * one workgroup runs through all keys.  Results are deterministic. */
+SVDQ_API int svdq_attention_workspace_size(int total_q, int total_k, int batch, int heads_q,
+                              int heads_k, int head_dim, size_t* out_bytes);
+SVDQ_API int svdq_attention(const void* q, const void* k, const void* v, void* o, float* lse,
+                              const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                              int batch, int total_q, int total_k, int heads_q, int heads_k,
+                              int head_dim, const int64_t* strides, float scale, int causal,
+                              int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Measurement hook: the dense matrix-core rate this GPU sustains.  Each of
  * `blocks` workgroups (4 waves; launch two per CU) issues 8 * iters
  * independent v_mfma_scale_f32_32x32x64_f8f6f4 per wave, with FP8 operands

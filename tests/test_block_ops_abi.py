@@ -1,0 +1,67 @@
+"""The 16-bit operators' C entry points refuse bad arguments before anything
+is launched."""
+
+import ctypes
+import math
+
+import pytest
+
+import bit_quantized_diffusion_amd as bq
+
+FAKE = ctypes.c_void_p(0x10000)      # aligned, never dereferenced (validation fails first)
+MIS = ctypes.c_void_p(0x10004)       # misaligned
+ODD = ctypes.c_void_p(0x10002)
+BAD, SHAPE = bq.SVDQ_ERR_INVALID_ARG, bq.SVDQ_ERR_SHAPE
+
+
+def _gpu_present():
+    import torch
+    return torch.cuda.is_available()
+
+
+ATTENTION = dict(q=FAKE, k=FAKE, v=FAKE, o=FAKE, lse=None, cu_q=FAKE, cu_k=FAKE, batch=2, tq=10, tk=20, hq=4, hk=2, d=64,
+                 strides=(256, 64, 128, 64, 128, 64, 256, 64), scale=0.125, causal=0, dtype=0, ws=None, n=0)
+
+
+def attention(**kw):
+    a = dict(ATTENTION, **kw)
+    strides = None if a["strides"] is None else (ctypes.c_int64 * 8)(*a["strides"])
+    return bq.lib.svdq_attention(a["q"], a["k"], a["v"], a["o"], a["lse"], a["cu_q"], a["cu_k"], a["batch"], a["tq"], a["tk"],
+                                 a["hq"], a["hk"], a["d"], strides, a["scale"], a["causal"], a["dtype"], a["ws"], a["n"], None)
+
+
+def with_stride(i, value):
+    s = list(ATTENTION["strides"])
+    s[i] = value
+    return tuple(s)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(q=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD), (dict(o=None), BAD), (dict(q=MIS), BAD), (dict(k=MIS), BAD),
+    (dict(v=MIS), BAD), (dict(o=MIS), BAD), (dict(ws=MIS), BAD), (dict(lse=ODD), BAD), (dict(cu_q=ODD), BAD),
+    (dict(cu_q=None), BAD), (dict(cu_k=None), BAD), (dict(cu_q=None, cu_k=None), BAD), (dict(strides=None), BAD),
+    (dict(strides=with_stride(0, 252)), BAD), (dict(strides=with_stride(3, -64)), BAD), (dict(strides=with_stride(2, 56)), BAD),
+    (dict(strides=with_stride(4, (1 << 23) + 8)), BAD), (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD),
+    (dict(scale=math.nan), BAD), (dict(scale=math.inf), BAD), (dict(dtype=2), BAD),
+    (dict(batch=0), SHAPE), (dict(tq=-1), SHAPE), (dict(tk=-1), SHAPE), (dict(hq=0), SHAPE), (dict(hk=3), SHAPE), (dict(hk=0), SHAPE),
+    (dict(d=0), SHAPE), (dict(d=60), SHAPE), (dict(d=136), SHAPE), (dict(tq=2 ** 31 - 1, hq=64, hk=2), SHAPE),
+    (dict(tq=2 ** 30, hq=64, hk=64), SHAPE),
+])
+def test_attention_refuses(kw, want):
+    assert attention(**kw) == want
+
+
+def test_attention_workspace_size():
+    f = bq.lib.svdq_attention_workspace_size
+    out = ctypes.c_size_t(7)
+    assert f(1, 1, 1, 1, 1, 64, None) == BAD
+    assert f(1, 1, 1, 3, 2, 64, ctypes.byref(out)) == SHAPE and out.value == 0
+    assert bq.attention_workspace_size(4608, 4608, 1, 24, 24, 128) == 0
+    # one token: parts of [heads][128 values + 2] fp32
+    n = bq.attention_workspace_size(1, 8192, 1, 8, 8, 128)
+    assert n > 0 and n % (8 * 130 * 4) == 0
+
+
+@pytest.mark.skipif(_gpu_present(), reason="checks the no-device path")
+def test_no_device():
+    assert attention() == bq.SVDQ_ERR_UNSUPPORTED_DEVICE
