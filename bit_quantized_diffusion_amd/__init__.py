@@ -23,7 +23,8 @@ import numpy as np
 from ._lib import (BF16, F16, INT4, MXFP4, SVDQ_ERR_HIP, SVDQ_ERR_INVALID_ARG,  # noqa: F401
                    SVDQ_ERR_SHAPE, SVDQ_ERR_UNSUPPORTED_DEVICE, SVDQ_OK,
                    EXPORTED, LIB_PATH, SvdqError, check, lib, status_string)
-from .block_ops import attention, attention_workspace_size  # noqa: F401
+from .block_ops import (attention, attention_workspace_size, layer_norm, linear16,  # noqa: F401
+                        linear16_workspace_size)
 
 __all__ = [
     "INT4", "MXFP4", "SvdqError", "lib", "LIB_PATH", "status_string", "merge_lora",
@@ -32,7 +33,8 @@ __all__ = [
     "unfused_linear_noalloc", "NOALLOC_SCRATCH_BYTES",
     "PackedLinear", "linear", "gemm_w4a4_lora_up_gelu", "mlp_gemm_gelu_quant", "mlp",
     "pack_w4a16", "gemm_w4a16", "mfma_ceiling",
-    "BF16", "F16", "attention", "attention_workspace_size",
+    "BF16", "F16", "attention", "attention_workspace_size", "linear16",
+    "linear16_workspace_size", "layer_norm",
 ]
 
 

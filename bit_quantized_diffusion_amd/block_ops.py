@@ -134,3 +134,116 @@ def attention(q, k, v, *, cu_seqlens_q=None, cu_seqlens_k=None, causal: bool = F
           _ptr(cu_seqlens_k), batch, total_q, total_k, heads_q, heads_k, head_dim, strides,
           head_dim ** -0.5 if scale is None else float(scale), int(bool(causal)), dtype, ws, ws_bytes)
     return (out, lse) if return_lse else out
+
+
+ACTIVATIONS = {"none": 0, "gelu": 1, "silu": 2}
+
+
+@functools.lru_cache(maxsize=4096)
+def linear16_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes of workspace with which `linear16` cuts small grids along K (0:
+    it runs them in one piece anyway)."""
+    out = ctypes.c_size_t(0)
+    check(lib.svdq_linear16_workspace_size(M, N, K, ctypes.byref(out)))
+    return int(out.value)
+
+
+def _ld(t):
+    """Row stride of a matrix (a single row has none, and gets its length)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _grouped(t, ref, rows, width, group_rows, name):
+    """A per-group matrix [groups][width] or one vector [width]: checked
+    against the rows it has to cover."""
+    if isinstance(t, torch.Tensor) and t.dim() == 1:
+        t = t.unsqueeze(0)
+        group_rows = max(rows, 1)
+    _like(t, ref, None, name)
+    if t.dim() != 2 or t.shape[1] != width:
+        raise ValueError(f"{name}: expected [groups][{width}] or [{width}], got {tuple(t.shape)}")
+    if group_rows is None:
+        if rows % t.shape[0]:
+            raise ValueError(f"{name}: {rows} rows do not divide into {t.shape[0]} groups; pass group_rows")
+        group_rows = rows // t.shape[0]
+    if group_rows < 1 or -(-rows // group_rows) > t.shape[0]:
+        raise ValueError(f"{name}: {t.shape[0]} groups of {group_rows} rows do not cover {rows} rows")
+    return t, group_rows
+
+
+def linear16(x, w, bias=None, *, activation: str = "none", gate=None, residual=None, group_rows=None, out=None,
+             workspace="auto"):
+    """residual + gate * act(x w^T + bias) in 16 bits with fp32 arithmetic
+    and one rounding.
+
+    x [M][K], w [N][K] (nn.Linear layout), bias [N], residual [M][N]; gate
+    [N], or [groups][N] with row r taking group r // group_rows (group_rows
+    defaults to M / groups).  activation: "none", "gelu" (tanh form) or
+    "silu".  Rows may be strided.  `out` may be `residual`."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
+        raise TypeError("x: expected a device tensor [M][K]")
+    dtype = _dtype_code(x, "x")
+    _like(x, x, None, "x")
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise TypeError("w: expected a device tensor [N][K]")
+    M, K = x.shape
+    N = w.shape[0]
+    _like(w, x, (N, K), "w")
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation: expected one of {tuple(ACTIVATIONS)}, got {activation!r}")
+    if bias is not None:
+        _like(bias, x, (N,), "bias")
+    rows = 1
+    if gate is not None:
+        gate, rows = _grouped(gate, x, M, N, group_rows, "gate")
+    if residual is not None:
+        _like(residual, x, (M, N), "residual")
+    if out is None:
+        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+    else:
+        _like(out, x, (M, N), "out")
+    if M == 0:
+        return out
+    nbytes = linear16_workspace_size(M, N, K) if isinstance(workspace, str) else 0
+    ws, ws_bytes, _keep = _workspace(workspace, nbytes, x.device)
+    _call(x.device, lib.svdq_linear16, _ptr(x), _ld(x), _ptr(w), _ld(w), _ptr(bias), _ptr(gate),
+          0 if gate is None else _ld(gate), rows, _ptr(residual), 0 if residual is None else _ld(residual), _ptr(out),
+          _ld(out), M, N, K, act, dtype, ws, ws_bytes)
+    return out
+
+
+def layer_norm(x, weight=None, bias=None, *, scale=None, shift=None, group_rows=None, eps: float = 1e-6, out=None):
+    """Adaptive layer norm over the last dimension of x [M][K]:
+    (x - mean) rstd [* weight + bias] [* (1 + scale) + shift], fp32 arithmetic,
+    one rounding.
+
+    weight, bias [K]; scale, shift [K], or [groups][K] with row r taking group
+    r // group_rows (group_rows defaults to M / groups).  Rows may be
+    strided.  `out` may be x."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
+        raise TypeError("x: expected a device tensor [M][K]")
+    dtype = _dtype_code(x, "x")
+    _like(x, x, None, "x")
+    M, K = x.shape
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _like(t, x, (K,), name)
+    rows, ld = 1, 0
+    if scale is not None:
+        scale, rows = _grouped(scale, x, M, K, group_rows, "scale")
+        ld = _ld(scale)
+    if shift is not None:
+        shift, shift_rows = _grouped(shift, x, M, K, group_rows, "shift")
+        if scale is not None and (shift_rows != rows or (_ld(shift) != ld and scale.shape[0] > 1)):
+            raise ValueError("scale and shift must have the same groups and row stride")
+        rows, ld = shift_rows, max(ld, _ld(shift))
+    if out is None:
+        out = torch.empty((M, K), dtype=x.dtype, device=x.device)
+    else:
+        _like(out, x, (M, K), "out")
+    if M == 0:
+        return out
+    _call(x.device, lib.svdq_layer_norm, _ptr(x), _ld(x), _ptr(weight), _ptr(bias), _ptr(scale), _ptr(shift), ld, rows,
+          _ptr(out), _ld(out), M, K, float(eps), dtype)
+    return out

@@ -36,7 +36,7 @@ DEVICE_FLAGS = [
 HOST_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-pthread",
               "-Wall", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", f"-I{ROCM}/include"]
 
-KERNEL_SOURCES = ["svdq_kernels.hip", "svdq_attention.hip"]
+KERNEL_SOURCES = ["svdq_kernels.hip", "svdq_attention.hip", "svdq_linear16.hip", "svdq_norm.hip"]
 HOST_SOURCES = ["svdq_abi.cpp", "svdq_pack.cpp"]
 
 

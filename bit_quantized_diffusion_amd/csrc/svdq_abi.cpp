@@ -58,6 +58,17 @@ int check_attention_shape(int total_q, int total_k, int batch, int heads_q, int 
   return SVDQ_OK;
 }
 
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+int check_linear16_shape(int M, int N, int K) {
+  if (M < 1 || N < 1 || K < 1) return SVDQ_ERR_SHAPE;
+  // tiles of 128 x 128 (32 channels for few rows) and 8-channel pieces of
+  // the result are counted in 31 bits
+  const long long m = M, n = N;
+  if (((m + 127) / 128) * ((n + 127) / 128) >= 1LL << 31 || ((n + 7) / 8) * m >= 1LL << 39) return SVDQ_ERR_SHAPE;
+  return SVDQ_OK;
+}
+
 int hip_status(int e) { return e == 0 ? SVDQ_OK : SVDQ_ERR_HIP; }
 
 }  // namespace
@@ -338,6 +349,51 @@ int svdq_attention(const void* q, const void* k, const void* v, void* o, float* 
   return hip_status(svdq_launch_attention(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, batch, total_q, total_k, heads_q,
                                           heads_k, head_dim, own, scale, causal != 0, dtype, workspace,
                                           workspace_bytes, stream));
+}
+
+int svdq_linear16_workspace_size(int M, int N, int K, size_t* out_bytes) {
+  if (!out_bytes) return SVDQ_ERR_INVALID_ARG;
+  *out_bytes = 0;
+  const int st = check_linear16_shape(M, N, K);
+  if (st) return st;
+  *out_bytes = svdq_linear16_plan_bytes(M, N, K);
+  return SVDQ_OK;
+}
+
+int svdq_linear16(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const void* gate,
+                  int64_t ld_gate, int group_rows, const void* residual, int64_t ldr, void* y, int64_t ldy, int M, int N,
+                  int K, int activation, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_dtype(dtype);
+  if (st) return st;
+  if (activation != SVDQ_ACT_NONE && activation != SVDQ_ACT_GELU && activation != SVDQ_ACT_SILU)
+    return SVDQ_ERR_INVALID_ARG;
+  if ((st = check_linear16_shape(M, N, K))) return st;
+  if (!x || !w || !y) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned2(x) || !aligned2(w) || !aligned2(y) || !aligned2(bias) || !aligned2(gate) || !aligned2(residual) ||
+      !aligned16(workspace))
+    return SVDQ_ERR_INVALID_ARG;
+  constexpr int64_t kMostLd = 1 << 22;
+  if (ldx < K || ldw < K || ldx > kMostLd || ldw > kMostLd || ldy < N || (residual && ldr < N)) return SVDQ_ERR_SHAPE;
+  if (gate && (ld_gate < N || group_rows < 1)) return SVDQ_ERR_SHAPE;
+  if ((st = current_device_ok())) return st;
+  return hip_status(svdq_launch_linear16(x, ldx, w, ldw, bias, gate, ld_gate, group_rows, residual, ldr, y, ldy, M, N, K,
+                                         activation, dtype, workspace, workspace_bytes, stream));
+}
+
+int svdq_layer_norm(const void* x, int64_t ldx, const void* weight, const void* bias, const void* scale,
+                    const void* shift, int64_t ld_mod, int group_rows, void* y, int64_t ldy, int M, int K, float eps,
+                    int dtype, void* stream) {
+  int st = check_dtype(dtype);
+  if (st) return st;
+  if (!x || !y) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned2(x) || !aligned2(y) || !aligned2(weight) || !aligned2(bias) || !aligned2(scale) || !aligned2(shift))
+    return SVDQ_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || std::isinf(eps)) return SVDQ_ERR_INVALID_ARG;
+  if (M < 1 || K < 1 || K > 65536 || ldx < K || ldy < K) return SVDQ_ERR_SHAPE;
+  if ((scale || shift) && (ld_mod < K || group_rows < 1)) return SVDQ_ERR_SHAPE;
+  if ((st = current_device_ok())) return st;
+  return hip_status(svdq_launch_layer_norm(x, ldx, weight, bias, scale, shift, ld_mod, group_rows < 1 ? 1 : group_rows, y,
+                                           ldy, M, K, eps, dtype, stream));
 }
 
 int svdq_bench_mfma_ceiling(int precision, int blocks, int iters, float* out, void* stream) {

@@ -111,6 +111,43 @@ __device__ __forceinline__ float other_half(float v) {
   return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
 }
 
+// 8 elements at any 2-byte aligned address (global memory takes unaligned
+// 16-byte accesses); the first `count` of them, the others zero
+__device__ __forceinline__ v4u load8(const uint16_t* p) {
+  v4u v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+__device__ __forceinline__ v4u load8(const uint16_t* p, int count) {
+  if (count >= 8) return load8(p);
+  v4u v = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (e < count) v[e >> 1] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
+  return v;
+}
+__device__ __forceinline__ void store8(uint16_t* p, v4u v, int count) {
+  if (count >= 8) {
+    __builtin_memcpy(p, &v, 16);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (e < count) p[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
+}
+template <typename E>
+__device__ __forceinline__ void unpack8(v4u v, float (&f)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[2 * e] = E::lo(v[e]);
+    f[2 * e + 1] = E::hi(v[e]);
+  }
+}
+template <typename E>
+__device__ __forceinline__ v4u pack8(const float (&f)[8]) {
+  return v4u{E::pack2(f[0], f[1]), E::pack2(f[2], f[3]), E::pack2(f[4], f[5]), E::pack2(f[6], f[7])};
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 }  // namespace svdq_dev

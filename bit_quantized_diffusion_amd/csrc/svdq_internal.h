@@ -85,6 +85,14 @@ int svdq_launch_attention(const void* q, const void* k, const void* v, void* o, 
                           const int32_t* cu_k, int batch, int total_q, int total_k, int heads_q, int heads_k,
                           int head_dim, const int64_t* strides, float scale, int causal, int dtype, void* workspace,
                           size_t workspace_bytes, void* stream);
+// Workspace bytes of svdq_launch_linear16 for these sizes (0: no split).
+size_t svdq_linear16_plan_bytes(int M, int N, int K);
+int svdq_launch_linear16(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const void* gate,
+                         int64_t ld_gate, int group_rows, const void* residual, int64_t ldr, void* y, int64_t ldy, int M,
+                         int N, int K, int activation, int dtype, void* workspace, size_t workspace_bytes, void* stream);
+int svdq_launch_layer_norm(const void* x, int64_t ldx, const void* weight, const void* bias, const void* scale,
+                           const void* shift, int64_t ld_mod, int group_rows, void* y, int64_t ldy, int M, int K,
+                           float eps, int dtype, void* stream);
 int svdq_launch_mfma_ceiling(int precision, int blocks, int iters, float* out, void* stream);
 int svdq_launch_unfused_linear_noalloc(const void* x, int M, int K, const float* smooth_inv, const void* lora_down,
                                        int rank, const uint8_t* wq, const void* ws, const void* lora_up,

@@ -367,6 +367,58 @@ SVDQ_API int svdq_attention(const void* q, const void* k, const void* v, void* o
                               int head_dim, const int64_t* strides, float scale, int causal,
                               int dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/* 16-bit linear with its epilogue, for the layers that stay in 16 bits
+ * (embedders, modulation, output projections):
+ *
+ *   y = residual + gate_g * act(x W^T + bias),   g = row / group_rows
+ *
+ *   x        (dev) [M][K], row stride ldx
+ *   w        (dev) [N][K] (nn.Linear layout), row stride ldw
+ *   bias     (dev) [N], or NULL
+ *   gate     (dev) [ceil(M / group_rows)][N], row stride ld_gate, or NULL
+ *   residual (dev) [M][N], row stride ldr, or NULL; may be y itself
+ *   y        (dev) [M][N], row stride ldy, out
+ * Products accumulate in fp32; bias, activation, gate and residual are
+ * applied in fp32 and y is rounded once.  activation: SVDQ_ACT_NONE,
+ * SVDQ_ACT_GELU (the tanh form, as in svdq_gemm_w4a4_lora_up_gelu) or
+ * SVDQ_ACT_SILU (z / (1 + exp(-z))).
+ * M, N, K >= 1, any values; strides in elements, at least the row's length
+ * and at most 2^22 for x and w; group_rows >= 1.  Pointers need 2-byte
+ * alignment only; rows of x and w that are 16-byte aligned with
+ * K % 8 == 0 take the faster loads.
+ * workspace (dev, 16-byte aligned): with the bytes that
+ * svdq_linear16_workspace_size names, grids that would leave the device
+ * idle are cut along K into fp32 parts that a second kernel adds in a fixed
+ * order; with NULL or fewer bytes they run in one piece.  Results are
+ * deterministic. */
+#define SVDQ_ACT_NONE  0
+#define SVDQ_ACT_GELU  1
+#define SVDQ_ACT_SILU  2
+SVDQ_API int svdq_linear16_workspace_size(int M, int N, int K, size_t* out_bytes);
+SVDQ_API int svdq_linear16(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+                              const void* gate, int64_t ld_gate, int group_rows,
+                              const void* residual, int64_t ldr, void* y, int64_t ldy,
+                              int M, int N, int K, int activation, int dtype,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Adaptive layer norm, the input of a block's projections:
+ *
+ *   y = (x - mean) rstd [* weight + bias] [* (1 + scale_g) + shift_g],
+ *   rstd = 1 / sqrt(var + eps),   g = row / group_rows
+ *
+ * with mean and (biased) variance of the row's K values in fp32, the
+ * variance taken from the deviations; y is rounded once.
+ *   x, y           (dev) [M][K], row strides ldx, ldy >= K; y may be x
+ *   weight, bias   (dev) [K], each or both NULL
+ *   scale, shift   (dev) [ceil(M / group_rows)][K], row stride ld_mod >= K,
+ *                  each or both NULL
+ * M >= 1; K from 1 to 65536; group_rows >= 1; eps >= 0 and finite.  Pointers
+ * need 2-byte alignment only. */
+SVDQ_API int svdq_layer_norm(const void* x, int64_t ldx, const void* weight, const void* bias,
+                              const void* scale, const void* shift, int64_t ld_mod, int group_rows,
+                              void* y, int64_t ldy, int M, int K, float eps, int dtype,
+                              void* stream);
+
 /* Measurement hook: the dense matrix-core rate this GPU sustains.  Each of
  * `blocks` workgroups (4 waves; launch two per CU) issues 8 * iters
  * independent v_mfma_scale_f32_32x32x64_f8f6f4 per wave, with FP8 operands

@@ -71,3 +71,81 @@ def assert_within(got, want, bound, what):
         i = tuple(int(x) for x in bad.nonzero()[0])
         raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} outside the bound, first at {i}: "
                              f"{float(got[i])} against {float(want[i])}, bound {float(bound[i])}")
+
+
+def _group_rows(t, rows, group_rows):
+    """Row-wise view of a per-group matrix or of one vector."""
+    t = t.detach().cpu().double()
+    return t.expand(rows, -1) if t.dim() == 1 else t[torch.arange(rows) // group_rows]
+
+
+def linear16_reference(x, w, bias, act, gate, residual, group_rows):
+    """(y, bound) in float64 on the CPU.
+
+    The sum of K products is off by at most K u32 sum |x||w| plus the bias's
+    rounding; both activations have slopes of at most 1.13 and are evaluated
+    to a few u32 of their argument's exponent (the exponential's argument is
+    rounded: |t| u32 relative); gate and residual add one rounding each, the
+    output one of 16 bits."""
+    dtype = x.dtype
+    u, tiny = U16[dtype], TINY[dtype]
+    x, w = x.detach().cpu().double(), w.detach().cpu().double()
+    z = x @ w.T
+    mag = x.abs() @ w.abs().T
+    if bias is not None:
+        z = z + bias.detach().cpu().double()
+        mag = mag + bias.detach().cpu().double().abs()
+    dz = (x.shape[1] + 2) * U32 * mag
+    if act == "gelu":
+        arg = 2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+        y = z * torch.sigmoid(arg)
+    elif act == "silu":
+        arg = z
+        y = z * torch.sigmoid(z)
+    else:
+        arg, y = torch.zeros_like(z), z
+    # past |arg| = 100 the exponential's own size (e^-100) bounds what is left
+    dy = (1.13 * dz if act != "none" else dz) + (8 * U32 + 6 * U32 * arg.abs().clamp(max=100)) * y.abs() + 2.0 ** -126
+    if gate is not None:
+        g = _group_rows(gate, x.shape[0], group_rows)
+        y, dy = y * g, dy * g.abs() + 2 * U32 * (y * g).abs()
+    if residual is not None:
+        r = residual.detach().cpu().double()
+        y, dy = y + r, dy + 2 * U32 * (y.abs() + r.abs())
+    return y, dy + u * (y.abs() + dy) + tiny
+
+
+def layer_norm_reference(x, weight, bias, scale, shift, group_rows, eps):
+    """(y, bound) in float64 on the CPU.
+
+    The mean is off by at most (log-tree or chunk) K u32 mean|x|; a deviation
+    by that and its own rounding; rstd by the relative error of the
+    variance's sum (K u32) and of what the deviations carry into it; each
+    product and sum after it rounds once."""
+    dtype = x.dtype
+    u, tiny = U16[dtype], TINY[dtype]
+    x = x.detach().cpu().double()
+    M, K = x.shape
+    mean = x.mean(1, keepdim=True)
+    off = x - mean
+    var = (off * off).mean(1, keepdim=True)
+    rstd = 1 / torch.sqrt(var + eps)
+    d_mean = (K + 2) * U32 * x.abs().mean(1, keepdim=True)
+    d_off = d_mean + 2 * U32 * (off.abs() + d_mean)
+    # variance: 2 E|off| d_mean + d_mean^2 and the sum's own rounding
+    d_var = 2 * off.abs().mean(1, keepdim=True) * d_mean + d_mean ** 2 + (K + 4) * U32 * (var + eps)
+    rel = d_var / (2 * (var + eps)) + 6 * U32
+    y = off * rstd
+    dy = d_off * rstd * (1 + rel) + y.abs() * (rel + 2 * U32)
+    for t, op in ((weight, "*"), (bias, "+"), (scale, "1*"), (shift, "+")):
+        if t is None:
+            continue
+        t = _group_rows(t, M, group_rows)
+        if op == "+":
+            y = y + t
+            dy = dy + 2 * U32 * (y.abs() + t.abs() + dy)
+        else:
+            t = t + 1 if op == "1*" else t
+            dy = dy * t.abs() * (1 + 4 * U32) + 4 * U32 * (y * t).abs()
+            y = y * t
+    return y, dy + u * (y.abs() + dy) + tiny

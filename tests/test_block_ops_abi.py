@@ -65,3 +65,44 @@ def test_attention_workspace_size():
 @pytest.mark.skipif(_gpu_present(), reason="checks the no-device path")
 def test_no_device():
     assert attention() == bq.SVDQ_ERR_UNSUPPORTED_DEVICE
+
+
+LINEAR = dict(x=FAKE, ldx=64, w=FAKE, ldw=64, bias=FAKE, gate=FAKE, ld_gate=32, rows=4, residual=FAKE, ldr=32, y=FAKE, ldy=32,
+              m=8, n=32, k=64, act=0, dtype=0, ws=None, size=0)
+NORM = dict(x=FAKE, ldx=64, weight=FAKE, bias=FAKE, scale=FAKE, shift=FAKE, ld=64, rows=4, y=FAKE, ldy=64, m=8, k=64, eps=1e-6,
+            dtype=0)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), BAD), (dict(w=None), BAD), (dict(y=None), BAD), (dict(x=ctypes.c_void_p(0x10001)), BAD),
+    (dict(residual=ctypes.c_void_p(0x10001)), BAD), (dict(ws=MIS), BAD), (dict(act=3), BAD), (dict(dtype=-1), BAD),
+    (dict(m=0), SHAPE), (dict(n=0), SHAPE), (dict(k=0), SHAPE), (dict(ldx=63), SHAPE), (dict(ldw=63), SHAPE), (dict(ldy=31), SHAPE),
+    (dict(ldr=31), SHAPE), (dict(ld_gate=31), SHAPE), (dict(rows=0), SHAPE), (dict(ldx=(1 << 22) + 1), SHAPE),
+])
+def test_linear16_refuses(kw, want):
+    assert bq.lib.svdq_linear16(*dict(LINEAR, **kw).values(), None) == want
+
+
+def test_linear16_workspace_size():
+    f = bq.lib.svdq_linear16_workspace_size
+    out = ctypes.c_size_t(7)
+    assert f(1, 1, 1, None) == BAD
+    assert f(0, 1, 1, ctypes.byref(out)) == SHAPE and out.value == 0
+    assert bq.linear16_workspace_size(4608, 12288, 3072) == 0
+    assert bq.linear16_workspace_size(100, 256, 4096) % (100 * 256 * 4) == 0
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), BAD), (dict(y=None), BAD), (dict(scale=ctypes.c_void_p(0x10001)), BAD), (dict(eps=-1.0), BAD),
+    (dict(eps=math.nan), BAD), (dict(eps=math.inf), BAD), (dict(dtype=5), BAD), (dict(m=0), SHAPE), (dict(k=0), SHAPE),
+    (dict(k=65537, ldx=65537, ldy=65537, ld=65537), SHAPE), (dict(ldx=63), SHAPE), (dict(ldy=63), SHAPE), (dict(ld=63), SHAPE),
+    (dict(rows=0), SHAPE),
+])
+def test_layer_norm_refuses(kw, want):
+    assert bq.lib.svdq_layer_norm(*dict(NORM, **kw).values(), None) == want
+
+
+@pytest.mark.skipif(_gpu_present(), reason="checks the no-device path")
+def test_no_device_linear16_and_norm():
+    assert bq.lib.svdq_linear16(*LINEAR.values(), None) == bq.SVDQ_ERR_UNSUPPORTED_DEVICE
+    assert bq.lib.svdq_layer_norm(*NORM.values(), None) == bq.SVDQ_ERR_UNSUPPORTED_DEVICE
