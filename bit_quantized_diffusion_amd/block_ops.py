@@ -13,26 +13,43 @@ import torch
 from ._lib import BF16, F16, check, lib
 
 _DTYPE = {torch.bfloat16: BF16, torch.float16: F16}
+_Strides = ctypes.c_int64 * 8
+
+# The smallest calls take about as long on the host as on the device, so the
+# arguments of a valid call are looked at once, cheaply; _refuse finds the
+# words for one that is not.
 
 
-def _dtype_code(t, name):
-    code = _DTYPE.get(t.dtype)
+def _operand(t, dims, name, layout):
+    """(dtype code, device index) of a call's first operand."""
+    try:
+        code, device = _DTYPE.get(t.dtype), t.get_device()
+        fine = t.dim() == dims and device >= 0 and (t.stride(-1) == 1 or t.shape[-1] <= 1)
+    except (AttributeError, RuntimeError):
+        raise TypeError(f"{name}: expected a device tensor {layout}") from None
     if code is None:
         raise TypeError(f"{name}: expected a bfloat16 or float16 tensor, got {t.dtype}")
-    return code
+    if not fine:
+        if t.dim() == dims and device >= 0:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+        raise TypeError(f"{name}: expected a device tensor {layout}")
+    return code, device
 
 
-def _like(t, ref, shape, name):
-    """`t` is a device tensor of ref's device and dtype, of this shape and
-    with a dense last dimension."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name}: expected a device tensor")
-    if t.dtype != ref.dtype or t.device != ref.device:
-        raise TypeError(f"{name}: expected {ref.dtype} on {ref.device}, got {t.dtype} on {t.device}")
-    if shape is not None and t.shape != shape:
+def _like(t, dtype, device, shape, name):
+    """`t` is a tensor of this dtype, device and shape with a dense last
+    dimension."""
+    try:
+        if (t.dtype is dtype and t.get_device() == device and t.shape == shape
+                and (t.stride(-1) == 1 or shape[-1] <= 1)):
+            return
+    except (AttributeError, RuntimeError):
+        raise TypeError(f"{name}: expected a device tensor") from None
+    if t.dtype is not dtype or t.get_device() != device:
+        raise TypeError(f"{name}: expected {dtype} on cuda:{device}, got {t.dtype} on {t.device}")
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
+    raise ValueError(f"{name}: the last dimension must be contiguous")
 
 
 def _ptr(t):
@@ -41,24 +58,32 @@ def _ptr(t):
 
 def _call(device, fn, *args):
     """Run a library call with `device` current, on its current stream."""
-    if device.index is not None and device.index != torch.cuda.current_device():
+    if device != torch.cuda.current_device():
         with torch.cuda.device(device):
-            return check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
-    check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        status = fn(*args, _raw_stream(device))
+    if status:
+        check(status)
+
+
+# the current stream's handle without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _workspace(workspace, nbytes, device):
     """(pointer, bytes, tensor kept alive): "auto" allocates on the call's
     stream, None gives none, a uint8 tensor is used as it is."""
+    if workspace is None:
+        return None, 0, None
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto', None or a uint8 device tensor")
         if not nbytes:
             return None, 0, None
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=device)
-    if workspace is None:
-        return None, 0, None
-    if workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=torch.device("cuda", device))
+    elif workspace.dtype != torch.uint8 or workspace.get_device() != device or not workspace.is_contiguous():
         raise TypeError("workspace: expected a contiguous uint8 tensor on the call's device")
     return workspace.data_ptr(), workspace.numel(), workspace
 
@@ -70,13 +95,6 @@ def attention_workspace_size(total_q: int, total_k: int, batch: int, heads_q: in
     out = ctypes.c_size_t(0)
     check(lib.svdq_attention_workspace_size(total_q, total_k, batch, heads_q, heads_k, head_dim, ctypes.byref(out)))
     return int(out.value)
-
-
-def _strides(t):
-    """Token and head strides; dimensions of size 1 have none, and get those
-    of a dense tensor."""
-    n, heads, d = t.shape
-    return (t.stride(0) if n > 1 else heads * d), (t.stride(1) if heads > 1 else d)
 
 
 def attention(q, k, v, *, cu_seqlens_q=None, cu_seqlens_k=None, causal: bool = False, scale=None, out=None,
@@ -96,44 +114,55 @@ def attention(q, k, v, *, cu_seqlens_q=None, cu_seqlens_k=None, causal: bool = F
     Returns o (like q, contiguous unless `out` is given) or, with
     return_lse, (o, lse fp32 [total_q][heads_q]).  A query that sees no key
     gives o = 0, lse = -inf."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
-        raise TypeError("q: expected a device tensor [tokens][heads][head_dim]")
-    dtype = _dtype_code(q, "q")
+    code, device = _operand(q, 3, "q", "[tokens][heads][head_dim]")
     total_q, heads_q, head_dim = q.shape
-    _like(q, q, None, "q")
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise TypeError("k: expected a device tensor [tokens][heads][head_dim]")
-    total_k, heads_k, _ = k.shape
-    _like(k, q, (total_k, heads_k, head_dim), "k")
-    _like(v, q, (total_k, heads_k, head_dim), "v")
+    _operand(k, 3, "k", "[tokens][heads][head_dim]")
+    total_k, heads_k, _ = shape = k.shape
+    dtype = q.dtype
+    _like(k, dtype, device, (total_k, heads_k, head_dim), "k")
+    _like(v, dtype, device, shape, "v")
     batch = 1
+    cu_q = cu_k = None
     if cu_seqlens_q is None:
         if cu_seqlens_k is not None:
             raise ValueError("cu_seqlens_k without cu_seqlens_q")
     else:
+        batch = _cu_seqlens(cu_seqlens_q, device, "cu_seqlens_q")
         if cu_seqlens_k is None:
             if total_k != total_q:
                 raise ValueError("cu_seqlens_k is needed where q and k have different numbers of tokens")
             cu_seqlens_k = cu_seqlens_q
-        for name, cu in (("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k)):
-            if cu.dtype != torch.int32 or cu.device != q.device or cu.dim() != 1 or not cu.is_contiguous():
-                raise TypeError(f"{name}: expected a contiguous int32 tensor [batch+1] on {q.device}")
-        batch = cu_seqlens_q.shape[0] - 1
-        if batch < 1 or cu_seqlens_k.shape[0] != batch + 1:
-            raise ValueError("cu_seqlens_q and cu_seqlens_k must both have batch + 1 >= 2 entries")
+        elif _cu_seqlens(cu_seqlens_k, device, "cu_seqlens_k") != batch:
+            raise ValueError("cu_seqlens_q and cu_seqlens_k must have the same number of entries")
+        cu_q, cu_k = cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr()
     if out is None:
-        out = torch.empty((total_q, heads_q, head_dim), dtype=q.dtype, device=q.device)
+        out = q.new_empty((total_q, heads_q, head_dim))
     else:
-        _like(out, q, q.shape, "out")
-    lse = torch.empty((total_q, heads_q), dtype=torch.float32, device=q.device) if return_lse else None
-    strides = (ctypes.c_int64 * 8)(*_strides(q), *_strides(k), *_strides(v), *_strides(out))
-    nbytes = attention_workspace_size(total_q, total_k, batch, heads_q, heads_k, head_dim) \
-        if isinstance(workspace, str) else 0
-    ws, ws_bytes, _keep = _workspace(workspace, nbytes, q.device)
-    _call(q.device, lib.svdq_attention, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens_q),
-          _ptr(cu_seqlens_k), batch, total_q, total_k, heads_q, heads_k, head_dim, strides,
-          head_dim ** -0.5 if scale is None else float(scale), int(bool(causal)), dtype, ws, ws_bytes)
+        _like(out, dtype, device, q.shape, "out")
+    lse = q.new_empty((total_q, heads_q), dtype=torch.float32) if return_lse else None
+    # token and head strides; dimensions of size 1 have none, and get those of a dense tensor
+    dense_q, dense_k = heads_q * head_dim, heads_k * head_dim
+    st = []
+    for t, n, h, dense in ((q, total_q, heads_q, dense_q), (k, total_k, heads_k, dense_k), (v, total_k, heads_k, dense_k),
+                           (out, total_q, heads_q, dense_q)):
+        a, b, _ = t.stride()
+        st += (a if n > 1 else dense, b if h > 1 else head_dim)
+    nbytes = 0 if workspace is None else attention_workspace_size(total_q, total_k, batch, heads_q, heads_k, head_dim)
+    ws, ws_bytes, _keep = _workspace(workspace, nbytes, device)
+    _call(device, lib.svdq_attention, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), cu_q, cu_k,
+          batch, total_q, total_k, heads_q, heads_k, head_dim, _Strides(*st),
+          head_dim ** -0.5 if scale is None else float(scale), 1 if causal else 0, code, ws, ws_bytes)
     return (out, lse) if return_lse else out
+
+
+def _cu_seqlens(cu, device, name):
+    """Number of sequences."""
+    if cu.dtype is not torch.int32 or cu.get_device() != device or cu.dim() != 1 or not cu.is_contiguous():
+        raise TypeError(f"{name}: expected a contiguous int32 tensor [batch+1] on cuda:{device}")
+    batch = cu.shape[0] - 1
+    if batch < 1:
+        raise ValueError(f"{name}: expected batch + 1 >= 2 entries")
+    return batch
 
 
 ACTIVATIONS = {"none": 0, "gelu": 1, "silu": 2}
@@ -153,22 +182,26 @@ def _ld(t):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-def _grouped(t, ref, rows, width, group_rows, name):
+def _grouped(t, dtype, device, rows, width, group_rows, name):
     """A per-group matrix [groups][width] or one vector [width]: checked
-    against the rows it has to cover."""
-    if isinstance(t, torch.Tensor) and t.dim() == 1:
-        t = t.unsqueeze(0)
-        group_rows = max(rows, 1)
-    _like(t, ref, None, name)
-    if t.dim() != 2 or t.shape[1] != width:
-        raise ValueError(f"{name}: expected [groups][{width}] or [{width}], got {tuple(t.shape)}")
+    against the rows it has to cover.  Returns (pointer, row stride, groups,
+    rows of a group)."""
+    try:
+        shape = t.shape
+    except AttributeError:
+        raise TypeError(f"{name}: expected a device tensor") from None
+    if len(shape) == 1:
+        _like(t, dtype, device, (width,), name)
+        return t.data_ptr(), width, 1, max(rows, 1)
+    _like(t, dtype, device, (shape[0], width) if len(shape) == 2 else (0, width), name)
+    groups = shape[0]
     if group_rows is None:
-        if rows % t.shape[0]:
-            raise ValueError(f"{name}: {rows} rows do not divide into {t.shape[0]} groups; pass group_rows")
-        group_rows = rows // t.shape[0]
-    if group_rows < 1 or -(-rows // group_rows) > t.shape[0]:
-        raise ValueError(f"{name}: {t.shape[0]} groups of {group_rows} rows do not cover {rows} rows")
-    return t, group_rows
+        if not groups or rows % groups:
+            raise ValueError(f"{name}: {rows} rows do not divide into {groups} groups; pass group_rows")
+        group_rows = max(rows // groups, 1)
+    if group_rows < 1 or -(-rows // group_rows) > groups:
+        raise ValueError(f"{name}: {groups} groups of {group_rows} rows do not cover {rows} rows")
+    return t.data_ptr(), t.stride(0) if groups > 1 else width, groups, group_rows
 
 
 def linear16(x, w, bias=None, *, activation: str = "none", gate=None, residual=None, group_rows=None, out=None,
@@ -180,36 +213,32 @@ def linear16(x, w, bias=None, *, activation: str = "none", gate=None, residual=N
     [N], or [groups][N] with row r taking group r // group_rows (group_rows
     defaults to M / groups).  activation: "none", "gelu" (tanh form) or
     "silu".  Rows may be strided.  `out` may be `residual`."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
-        raise TypeError("x: expected a device tensor [M][K]")
-    dtype = _dtype_code(x, "x")
-    _like(x, x, None, "x")
-    if not isinstance(w, torch.Tensor) or w.dim() != 2:
-        raise TypeError("w: expected a device tensor [N][K]")
+    code, device = _operand(x, 2, "x", "[M][K]")
+    _operand(w, 2, "w", "[N][K]")
     M, K = x.shape
     N = w.shape[0]
-    _like(w, x, (N, K), "w")
+    dtype = x.dtype
+    _like(w, dtype, device, (N, K), "w")
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation: expected one of {tuple(ACTIVATIONS)}, got {activation!r}")
     if bias is not None:
-        _like(bias, x, (N,), "bias")
-    rows = 1
-    if gate is not None:
-        gate, rows = _grouped(gate, x, M, N, group_rows, "gate")
+        _like(bias, dtype, device, (N,), "bias")
+    gate_ptr, ld_gate, _, rows = (None, 0, 1, 1) if gate is None else \
+        _grouped(gate, dtype, device, M, N, group_rows, "gate")
     if residual is not None:
-        _like(residual, x, (M, N), "residual")
+        _like(residual, dtype, device, (M, N), "residual")
     if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        out = x.new_empty((M, N))
     else:
-        _like(out, x, (M, N), "out")
+        _like(out, dtype, device, (M, N), "out")
     if M == 0:
         return out
-    nbytes = linear16_workspace_size(M, N, K) if isinstance(workspace, str) else 0
-    ws, ws_bytes, _keep = _workspace(workspace, nbytes, x.device)
-    _call(x.device, lib.svdq_linear16, _ptr(x), _ld(x), _ptr(w), _ld(w), _ptr(bias), _ptr(gate),
-          0 if gate is None else _ld(gate), rows, _ptr(residual), 0 if residual is None else _ld(residual), _ptr(out),
-          _ld(out), M, N, K, act, dtype, ws, ws_bytes)
+    nbytes = 0 if workspace is None else linear16_workspace_size(M, N, K)
+    ws, ws_bytes, _keep = _workspace(workspace, nbytes, device)
+    _call(device, lib.svdq_linear16, x.data_ptr(), _ld(x), w.data_ptr(), _ld(w), _ptr(bias), gate_ptr, ld_gate, rows,
+          _ptr(residual), 0 if residual is None else _ld(residual), out.data_ptr(), _ld(out), M, N, K, act, code, ws,
+          ws_bytes)
     return out
 
 
@@ -221,29 +250,28 @@ def layer_norm(x, weight=None, bias=None, *, scale=None, shift=None, group_rows=
     weight, bias [K]; scale, shift [K], or [groups][K] with row r taking group
     r // group_rows (group_rows defaults to M / groups).  Rows may be
     strided.  `out` may be x."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
-        raise TypeError("x: expected a device tensor [M][K]")
-    dtype = _dtype_code(x, "x")
-    _like(x, x, None, "x")
+    code, device = _operand(x, 2, "x", "[M][K]")
     M, K = x.shape
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _like(t, x, (K,), name)
-    rows, ld = 1, 0
+    dtype = x.dtype
+    if weight is not None:
+        _like(weight, dtype, device, (K,), "weight")
+    if bias is not None:
+        _like(bias, dtype, device, (K,), "bias")
+    scale_ptr = shift_ptr = None
+    rows, ld = 1, K
     if scale is not None:
-        scale, rows = _grouped(scale, x, M, K, group_rows, "scale")
-        ld = _ld(scale)
+        scale_ptr, ld, groups, rows = _grouped(scale, dtype, device, M, K, group_rows, "scale")
     if shift is not None:
-        shift, shift_rows = _grouped(shift, x, M, K, group_rows, "shift")
-        if scale is not None and (shift_rows != rows or (_ld(shift) != ld and scale.shape[0] > 1)):
+        shift_ptr, ld_shift, shift_groups, shift_rows = _grouped(shift, dtype, device, M, K, group_rows, "shift")
+        if scale is not None and (shift_rows != rows or shift_groups != groups or (ld_shift != ld and groups > 1)):
             raise ValueError("scale and shift must have the same groups and row stride")
-        rows, ld = shift_rows, max(ld, _ld(shift))
+        rows, ld = shift_rows, ld_shift
     if out is None:
-        out = torch.empty((M, K), dtype=x.dtype, device=x.device)
+        out = x.new_empty((M, K))
     else:
-        _like(out, x, (M, K), "out")
+        _like(out, dtype, device, (M, K), "out")
     if M == 0:
         return out
-    _call(x.device, lib.svdq_layer_norm, _ptr(x), _ld(x), _ptr(weight), _ptr(bias), _ptr(scale), _ptr(shift), ld, rows,
-          _ptr(out), _ld(out), M, K, float(eps), dtype)
+    _call(device, lib.svdq_layer_norm, x.data_ptr(), _ld(x), _ptr(weight), _ptr(bias), scale_ptr, shift_ptr, ld, rows,
+          out.data_ptr(), _ld(out), M, K, eps, code)
     return out
