@@ -23,10 +23,14 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 // The two 16-bit element types.  pack2 rounds two fp32 values to nearest
-// even; mfma is the 32x32x16 product with fp32 accumulation:
+// even; mfma is the 32x32x16 product with fp32 accumulation,
 //   A  lane l: row l % 32, k = 8 (l / 32) .. + 7
 //   B  lane l: column l % 32, the same k
-//   D  lane l, element 4 j + r: row 8 j + 4 (l / 32) + r, column l % 32.
+//   D  lane l, element 4 j + r: row 8 j + 4 (l / 32) + r, column l % 32,
+// mfma16 the 16x16x32 one:
+//   A  lane l: row l % 16, k = 8 (l / 16) .. + 7
+//   B  lane l: column l % 16, the same k
+//   D  lane l, element r: row 4 (l / 16) + r, column l % 16.
 struct Bf16 {
   static __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2bf));
@@ -35,6 +39,9 @@ struct Bf16 {
   static __device__ __forceinline__ float hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
   static __device__ __forceinline__ v16f mfma(v4u a, v4u b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ v4f mfma16(v4u a, v4u b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
   }
 };
 struct F16 {
@@ -49,6 +56,9 @@ struct F16 {
   }
   static __device__ __forceinline__ v16f mfma(v4u a, v4u b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ v4f mfma16(v4u a, v4u b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
   }
 };
 
@@ -78,6 +88,12 @@ __device__ __forceinline__ void dma_b128(__amdgpu_buffer_rsrc_t r, uint32_t lds,
                :: "v"(voff), "s"(r), "{m0}"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
 }
 
+// the same with a wave-uniform offset added to voff
+__device__ __forceinline__ void dma_b128(__amdgpu_buffer_rsrc_t r, uint32_t lds, int voff, int soff) {
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               :: "v"(voff), "s"(r), "s"(soff), "{m0}"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
+}
+
 // at most N of the wave's vector-memory loads outstanding
 template <int N>
 __device__ __forceinline__ void vm_wait() {
@@ -91,6 +107,19 @@ __device__ __forceinline__ void lds_wait_barrier() {
   static_assert(N >= 0 && N < 64, "vmcnt field");
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(N) : "memory");
 }
+
+// the same with the wave's last L LDS reads still in flight
+template <int N, int L>
+__device__ __forceinline__ void lds_wait_barrier() {
+  static_assert(N >= 0 && N < 64 && L >= 0 && L < 16, "vmcnt and lgkmcnt fields");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(%1)\n\ts_barrier" :: "n"(N), "n"(L) : "memory");
+}
+// the workgroup's LDS accesses done; memory loads and stores stay in flight
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// nothing is scheduled across this point
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+// memory operations stay on their side of this point
+__device__ __forceinline__ void order() { asm volatile("" ::: "memory"); }
 
 // 16 bytes of LDS at byte address a
 __device__ __forceinline__ v4u lds_read16(uint32_t a) {

@@ -9,7 +9,10 @@
 // results lie along n, the dense dimension of y.
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "svdq_device.h"
 #include "svdq_internal.h"
@@ -34,7 +37,7 @@ __device__ __forceinline__ float activate(float z, int act) {
   constexpr float kLog2e = 1.4426950408889634f;
   constexpr float kG = 2.f * 0.7978845608028654f * kLog2e;
   const float t = act == SVDQ_ACT_SILU ? z * kLog2e : z * (kG + kG * 0.044715f * z * z);
-  return z / (1.f + exp2_fast(-t));
+  return z * __builtin_amdgcn_rcpf(1.f + exp2_fast(-t));   // reciprocal within 1 ulp
 }
 
 // A lane's 8 consecutive channels of one row: the epilogue and the store.
@@ -73,182 +76,344 @@ struct Columns {
   }
 };
 
-// 16-byte chunk c of row r of a tile with 64 values a row (128 bytes; two
-// rows share the LDS banks) sits at chunk c ^ swz(r): the reads of one chunk
-// of 16 consecutive rows fall in distinct banks.
-__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
-
-// ---------------------------------------------------------------------------
-// Tiles of BN channels x BM rows, WN x WM waves, K in stages of 64.  DMA: both
-// operands come straight to LDS, double-buffered (needs 16-byte aligned rows
-// and K % 8 == 0); else through registers with unaligned loads.
-// ---------------------------------------------------------------------------
-
-template <typename E, int BN, int BM, int WN, int WM, bool DMA>
-__global__ __launch_bounds__(WN * WM * 64, 2) void k_linear16(LinArgs a) {
-  constexpr int kWaves = WN * WM;
-  constexpr int TN = BN / WN / 32, TM = BM / WM / 32;    // 32 x 32 tiles of a wave
-  constexpr int kRowB = 128;                             // bytes of a row and stage
-  constexpr int kStage = (BN + BM) * kRowB;
-  constexpr int kLoads = kStage / 1024 / kWaves;         // 1 KB (8 rows) each
-  static_assert(kStage % (1024 * kWaves) == 0, "loads divide evenly");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
-  static_assert(kWaves * 32 * TN * 32 * 4 <= 2 * kStage, "the epilogue's staging fits");
-
-  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wn = wave % WN, wm = wave / WN;
-
-  // tile: each XCD takes a contiguous range of tiles, walked in groups of 8
-  // rows of tiles, so that tiles that run together share operand panels
+// The tile of a workgroup: each XCD (consecutive ids go to consecutive XCDs)
+// takes a contiguous range of tiles, walked in groups of 8 rows of tiles, so
+// that tiles that run together share operand panels in its L2.
+template <int BN, int BM>
+__device__ __forceinline__ void tile_of(const LinArgs& a, int block, int& m0, int& n0) {
   const int tn = (a.N + BN - 1) / BN, tm = (a.M + BM - 1) / BM, tiles = tn * tm;
-  int id = blockIdx.x;
-  {
-    const int per = (tiles + 7) / 8, x = id & 7, full = tiles - 8 * (per - 1);   // the first `full` XCDs take `per`
-    id = (x < full ? x * per : full * per + (x - full) * (per - 1)) + (id >> 3);
-  }
+  const int per = (tiles + 7) / 8, x = block & 7, full = tiles - 8 * (per - 1);   // the first `full` XCDs take `per`
+  const int id = (x < full ? x * per : full * per + (x - full) * (per - 1)) + (block >> 3);
   const int group = id / (8 * tn), in = id - group * 8 * tn;
   const int gm = min(8, tm - group * 8);
-  const int m0 = (group * 8 + in % gm) * BM, n0 = in / gm * BN;
+  m0 = (group * 8 + in % gm) * BM;
+  n0 = in / gm * BN;
+}
 
+// Epilogue of a workgroup's BN x BM tile.  A wave holds TN x TM results of
+// 16 x 16 (lane l, element r: channel 4 (l / 16) + r, row l % 16).  JP of its
+// TM rows of tiles at a time go through LDS as [rows][BN] fp32, 16-byte chunk
+// c of row r at chunk c ^ (r % 16); then a thread takes 8 channels of a row,
+// always the same channels, and the threads together whole rows.  A tile that
+// lies inside the result, in rows that allow 16-byte accesses and in one
+// group, takes a loop without a check per row, its residual loaded
+// ahead; the others go through Columns.
+template <typename E, int BN, int BM, int WN, int WM, int TN, int TM, int JP>
+__device__ __forceinline__ void epilogue(const LinArgs& a, const v4f (&acc)[TN][TM], uint8_t* lds, int m0, int n0) {
+  constexpr int kThreads = WN * WM * 64, kC4 = BN / 4, kLanesRow = BN / 8, kPass = kThreads / kLanesRow;
+  constexpr int kRowsJ = JP * WM * 16, kIter = kRowsJ / kPass;
+  static_assert(kC4 % 16 == 0 && TM % JP == 0 && kThreads % kLanesRow == 0 && kRowsJ % kPass == 0 && true,
+                "the swizzle stays inside a row; whole passes");
+  float* const stage = reinterpret_cast<float*>(lds);
+  const int l16 = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3, wave = threadIdx.x >> 6;
+  const int wn = wave % WN, wm = wave / WN;
+  const int c8 = threadIdx.x % kLanesRow, r0 = threadIdx.x / kLanesRow;
+  const int nl = n0 + c8 * 8;
+  const bool wide = a.splits == 1 && m0 + BM <= a.M && n0 + BN <= a.N && (a.ldy & 7) == 0 && (a.ldr & 7) == 0 &&
+                    (!a.gate || m0 / a.group_rows == (m0 + BM - 1) / a.group_rows);
+  Columns<E> col;
+  if (a.splits == 1) col.init(a, nl);
+  if (wide && a.gate) unpack8<E>(load8(a.gate + m0 / a.group_rows * a.ld_gate + nl), col.gate);
+  // row of the tile that staged row r is, in pass jp
+  auto tile_row = [&](int jp, int r) { return (((r >> 4) % WM) * TM + jp + (r >> 4) / WM) * 16 + (r & 15); };
+  auto staged = [&](int r, float (&f)[8]) {
+    const v4f lo = *reinterpret_cast<const v4f*>(stage + (r * kC4 + ((2 * c8) ^ (r & 15))) * 4);
+    const v4f hi = *reinterpret_cast<const v4f*>(stage + (r * kC4 + ((2 * c8 + 1) ^ (r & 15))) * 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[e] = lo[e];
+      f[4 + e] = hi[e];
+    }
+  };
+#pragma unroll
+  for (int jp = 0; jp < TM; jp += JP) {
+    if (jp) lds_barrier();
+    v4u res[kIter];
+    const bool add = wide && a.residual;
+    if (add) {
+#pragma unroll
+      for (int it = 0; it < kIter; ++it)
+        res[it] = load8(a.residual + (m0 + tile_row(jp, r0 + it * kPass)) * a.ldr + nl);
+    }
+    // staged row (jj WM + wm) 16 + l16 is row (wm TM + jp + jj) 16 + l16 of the tile
+#pragma unroll
+    for (int jj = 0; jj < JP; ++jj)
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+        *reinterpret_cast<v4f*>(stage + (((jj * WM + wm) * 16 + l16) * kC4 + ((wn * TN * 4 + i * 4 + q) ^ l16)) * 4) =
+            acc[i][jp + jj];
+    lds_barrier();
+    if (wide) {
+#pragma unroll
+      for (int it = 0; it < kIter; ++it) {
+        const int r = r0 + it * kPass;
+        float f[8];
+        staged(r, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] += col.bias[e];
+        if (a.act != SVDQ_ACT_NONE) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = activate(f[e], a.act);
+        }
+        if (a.gate) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= col.gate[e];
+        }
+        if (add) {
+          float x[8];
+          unpack8<E>(res[it], x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] += x[e];
+        }
+        store8(a.y + (m0 + tile_row(jp, r)) * a.ldy + nl, pack8<E>(f), 8);
+      }
+    } else {
+#pragma unroll 1
+      for (int r = r0; r < kRowsJ; r += kPass) {
+        float f[8];
+        staged(r, f);
+        const int m = m0 + tile_row(jp, r);
+        if (a.splits == 1) {
+          col.finish(a, m, f);
+        } else if (m < a.M && nl < a.N) {
+          float* p = a.part + (static_cast<int64_t>(blockIdx.y) * a.M + m) * a.N + nl;
+          if (nl + 8 <= a.N && (a.N & 3) == 0) {
+            *reinterpret_cast<v4f*>(p) = v4f{f[0], f[1], f[2], f[3]};
+            *reinterpret_cast<v4f*>(p + 4) = v4f{f[4], f[5], f[6], f[7]};
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (nl + e < a.N) p[e] = f[e];
+          }
+        }
+      }
+    }
+  }
+}
+
+// rows of tiles that fit the epilogue's LDS at a time: the largest divisor of TM
+constexpr int staged_tiles(int TM, int row_bytes, int bytes) {
+  for (int j = TM; j > 1; --j)
+    if (TM % j == 0 && j * row_bytes <= bytes) return j;
+  return 1;
+}
+
+// ---------------------------------------------------------------------------
+// Tiles of BN channels x BM rows, WN x WM waves; rows 16-byte aligned and
+// K % 8 == 0.  K runs in stages of 64: whole 128-byte lines of the rows of W
+// and of x, that loads put straight into LDS, W in a ring of 3 + D slots, x
+// in one of 2 + D.  A stage's two steps of 32 k each read the next step's
+// operands from LDS between their products.  The one barrier of a stage
+// stands before its last step: by then the stage has been read out and the
+// next one has landed, so that the last step reads that one's first
+// operands.  W of stage + 2 + D is loaded in the first step, x in the last:
+// loads have 1 1/2 + D stages and one + D to arrive.  They are spread evenly
+// over the products: issued in one burst they block the wave (output
+// projection 69 -> 75 us).  D > 0 is for small grids, whose stages are
+// shorter than a load's way.
+// Products of 16 x 16 x 32: the chip runs this kernel at its power limit
+// (zeros 19 % faster than normal values), and they move fewer register bytes
+// per product than 32 x 32 x 16 (4608 x 12288 x 3072: 318 -> 298 us).
+// A row of a slot is 128 bytes, two rows share the LDS banks: 16-byte chunk c
+// of row r sits at chunk c ^ ((r / 2) % 8).
+// ---------------------------------------------------------------------------
+
+template <typename E, int BN, int BM, int WN, int WM, int D>
+__global__ __launch_bounds__(WN * WM * 64, 2) void k_linear16(LinArgs a) {
+  constexpr int kWaves = WN * WM;
+  constexpr int TN = BN / WN / 16, TM = BM / WM / 16, T = TN * TM;   // 16 x 16 tiles of a wave
+  constexpr int kRowB = 128, kReads = TN + TM;
+  // a wave's loads of a slot, 1 KB (8 rows) each; the last waves' may lie past the tile
+  constexpr int kLw = (BN / 8 + kWaves - 1) / kWaves, kLx = (BM / 8 + kWaves - 1) / kWaves;
+  constexpr int kSlotW = kLw * kWaves * 1024, kSlotX = kLx * kWaves * 1024, kX = (3 + D) * kSlotW;
+  constexpr int kLds = kX + (2 + D) * kSlotX;
+  static_assert(BN % (16 * WN) == 0 && BM % (16 * WM) == 0 && kReads <= T && kLw <= T && kLx <= T, "tiles divide evenly");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wave % WN, wm = wave / WN;
+  int m0, n0;
+  tile_of<BN, BM>(a, blockIdx.x, m0, n0);
   const int stages = (a.K + 63) / 64;
   const int s0 = blockIdx.y * a.stages_per_split, s1 = min(s0 + a.stages_per_split, stages);
 
   const uint32_t base = lds_addr(lds);
-  // load n of a wave: rows 8 (wave kLoads + n) .. + 7 of the BN + BM rows
-  int voff[kLoads];
+  const __amdgpu_buffer_rsrc_t bw = buffer_of(a.w + n0 * a.ldw, ((a.N - n0 - 1) * a.ldw + a.K) * 2);
+  const __amdgpu_buffer_rsrc_t bx = buffer_of(a.x + m0 * a.ldx, ((a.M - m0 - 1) * a.ldx + a.K) * 2);
+  // load n of a wave: rows 8 p .. 8 p + 7 of a slot, p = wave kL + n; the
+  // lane's chunk is (lane % 8) ^ (4 p + lane / 16) % 8
+  auto chunk = [&](int p) { return (lane & 7) ^ (((p & 1) << 2) + (lane >> 4)); };
+  int vw[kLw], vx[kLx];
 #pragma unroll
-  for (int n = 0; n < kLoads; ++n) {
-    const int r = (wave * kLoads + n) * 8 + (lane >> 3);
-    const bool is_x = r >= BN;
-    const int rr = is_x ? r - BN : r;
-    voff[n] = static_cast<int>(rr * (is_x ? a.ldx : a.ldw) * 2) + (((lane & 7) ^ swz(rr)) << 4);
+  for (int n = 0; n < kLw; ++n) {
+    const int r = (wave * kLw + n) * 8 + (lane >> 3);
+    vw[n] = r < BN ? static_cast<int>(r * a.ldw * 2) + (chunk(wave * kLw + n) << 4) : kOutside;
   }
-  auto issue = [&](int st, int buf) {
-    const int k0 = st * 64;
-    const uint16_t* const pw = a.w + n0 * a.ldw + k0;
-    const uint16_t* const px = a.x + m0 * a.ldx + k0;
-    const auto rw = buffer_of(pw, ((a.N - n0 - 1) * a.ldw + a.K - k0) * 2);
-    const auto rx = buffer_of(px, ((a.M - m0 - 1) * a.ldx + a.K - k0) * 2);
-    const bool tail = k0 + 64 > a.K;
 #pragma unroll
-    for (int n = 0; n < kLoads; ++n) {
-      const int r8 = wave * kLoads + n;
-      int vo = voff[n];
-      if (tail && k0 + ((lane & 7) ^ swz((r8 * 8 + (lane >> 3)) % BN)) * 8 >= a.K) vo = kOutside;
-      dma_b128(r8 * 8 >= BN ? rx : rw, base + buf * kStage + r8 * 1024, vo);
-    }
+  for (int n = 0; n < kLx; ++n) {
+    const int r = (wave * kLx + n) * 8 + (lane >> 3);
+    vx[n] = r < BM ? static_cast<int>(r * a.ldx * 2) + (chunk(wave * kLx + n) << 4) : kOutside;
+  }
+  // past K, rows would run on into the next
+  auto load_w = [&](int st, uint32_t slot, int n) {
+    const bool outside = st * 64 + chunk(wave * kLw + n) * 8 >= a.K;
+    dma_b128(bw, base + slot + (wave * kLw + n) * 1024, outside ? kOutside : vw[n], st * 128);
   };
-  v4u held[DMA ? 1 : kLoads];
+  auto load_x = [&](int st, uint32_t slot, int n) {
+    const bool outside = st * 64 + chunk(wave * kLx + n) * 8 >= a.K;
+    dma_b128(bx, base + slot + (wave * kLx + n) * 1024, outside ? kOutside : vx[n], st * 128);
+  };
+
+  // LDS offsets of the lane's operand reads: row, chunk 4 step + q
+  uint32_t rw[2], rx[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const uint32_t o = base + l16 * kRowB + (((4 * s + q) ^ (l16 >> 1)) << 4);
+    rw[s] = o + wn * TN * 16 * kRowB;
+    rx[s] = o + wm * TM * 16 * kRowB;
+  }
+  v4f acc[TN][TM];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  v4u f[2][kReads];   // operands of two steps, W's tiles then x's
+  // read i of a step: x's tiles first, the first products take all of them
+  auto read = [&](uint32_t sw, uint32_t sx, auto step, int i) {
+    constexpr int s = decltype(step)::value;
+    if (i < TM)
+      f[s][TN + i] = lds_read16(rx[s] + sx + i * 16 * kRowB);
+    else
+      f[s][i - TM] = lds_read16(rw[s] + sw + (i - TM) * 16 * kRowB);
+  };
+  // the products of step s, between them the reads of step s ^ 1 (slots sw,
+  // sx) and the `loads` loads that `issue` makes
+  auto step = [&](auto s_, uint32_t sw, uint32_t sx, auto loads, auto issue) {
+    constexpr int s = decltype(s_)::value, kL = decltype(loads)::value, kGap = T / kL;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      acc[t / TM][t % TM] = E::mfma16(f[s][t / TM], f[s][TN + t % TM], acc[t / TM][t % TM]);
+      if (t < kReads) read(sw, sx, std::integral_constant<int, s ^ 1>{}, t);
+      if (t % kGap == kGap - 1 && t / kGap < kL) issue(t / kGap);
+      fence();
+    }
+    order();
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+
+#pragma unroll
+  for (int i = 0; i < 2 + D; ++i)
+    if (s0 + i < s1) {
+#pragma unroll
+      for (int n = 0; n < kLw; ++n) load_w(s0 + i, i * kSlotW, n);
+#pragma unroll
+      for (int n = 0; n < kLx; ++n) load_x(s0 + i, kX + i * kSlotX, n);
+    }
+  if (s0 + 1 + D < s1)
+    lds_wait_barrier<(1 + D) * (kLw + kLx)>();
+  else
+    lds_wait_barrier<0>();
+#pragma unroll
+  for (int i = 0; i < kReads; ++i) read(0, kX, I0{}, i);
+  // slots of this stage; W's of the stage to load next
+  uint32_t ws = 0, xs = kX, wl = (2 + D) * kSlotW;
+  auto stage = [&](int st, auto more) {
+    constexpr bool kMore = decltype(more)::value;
+    step(I0{}, ws, xs, std::integral_constant<int, kLw>{}, [&](int n) {
+      if constexpr (kMore) load_w(st + 2 + D, wl, n);
+    });
+    // read out; stage st + 1 has landed, W of st + 2 + D and the stages between may fly
+    lds_wait_barrier<kMore ? kLw + D * (kLw + kLx) : 0>();
+    wl = ws;
+    ws = ws == (2 + D) * kSlotW ? 0 : ws + kSlotW;
+    const uint32_t x = xs;
+    xs = xs == kX + (1 + D) * kSlotX ? kX : xs + kSlotX;
+    // (past the last stage this reads a slot's old bytes, which are not used)
+    step(I1{}, ws, xs, std::integral_constant<int, kLx>{}, [&](int n) {
+      if constexpr (kMore) load_x(st + 2 + D, x, n);
+    });
+  };
+  int st = s0;
+  for (; st + 2 + D < s1; ++st) stage(st, std::true_type{});
+  for (; st < s1; ++st) stage(st, std::false_type{});
+  // the reads past the last stage are done before the staging overwrites LDS
+  lds_wait_barrier<0>();
+  epilogue<E, BN, BM, WN, WM, TN, TM, staged_tiles(TM, WM * 16 * BN * 4, kLds)>(a, acc, lds, m0, n0);
+}
+
+// ---------------------------------------------------------------------------
+// The same for rows at any 2-byte alignment and any K: tiles of 128 x 128,
+// stages of 64 fetched with unaligned loads into registers one stage ahead.
+// A row of a stage is 128 bytes, two rows share the LDS banks; chunk c of row
+// r sits at chunk c ^ ((r / 2) % 8).
+// ---------------------------------------------------------------------------
+
+template <typename E>
+__global__ __launch_bounds__(256, 2) void k_linear16_any(LinArgs a) {
+  constexpr int B = 128, kRowB = 128, kStage = 2 * B * kRowB, kLoads = kStage / 1024 / 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wave & 1, wm = wave >> 1;
+  int m0, n0;
+  tile_of<B, B>(a, blockIdx.x, m0, n0);
+  const int stages = (a.K + 63) / 64;
+  const int s0 = blockIdx.y * a.stages_per_split, s1 = min(s0 + a.stages_per_split, stages);
+
+  // load n of a wave: rows 8 (wave kLoads + n) .. + 7; waves 0, 1 take W, 2, 3 take x
+  const bool is_x = wave >= 2;
+  const uint16_t* const p = is_x ? a.x + m0 * a.ldx : a.w + n0 * a.ldw;
+  const int64_t ld = is_x ? a.ldx : a.ldw;
+  const int rows = is_x ? a.M - m0 : a.N - n0;
+  v4u held[kLoads];
   auto fetch = [&](int st) {
 #pragma unroll
     for (int n = 0; n < kLoads; ++n) {
-      const int r = (wave * kLoads + n) * 8 + (lane >> 3);
-      const bool is_x = r >= BN;
-      const int rr = is_x ? r - BN : r;
-      const int k = st * 64 + ((lane & 7) ^ swz(rr)) * 8;
-      held[DMA ? 0 : n] = v4u{0, 0, 0, 0};
-      const int64_t row = is_x ? m0 + rr : n0 + rr;
-      if (row < (is_x ? a.M : a.N) && k < a.K)
-        held[DMA ? 0 : n] = load8((is_x ? a.x + row * a.ldx : a.w + row * a.ldw) + k, a.K - k);
+      const int r = ((wave & 1) * kLoads + n) * 8 + (lane >> 3);
+      const int k = st * 64 + ((lane & 7) ^ ((r >> 1) & 7)) * 8;
+      held[n] = v4u{0, 0, 0, 0};
+      if (r < rows && k < a.K) held[n] = load8(p + r * ld + k, a.K - k);
     }
   };
   auto put = [&](int buf) {
 #pragma unroll
     for (int n = 0; n < kLoads; ++n)
-      *reinterpret_cast<v4u*>(lds + buf * kStage + (wave * kLoads + n) * 1024 + lane * 16) = held[DMA ? 0 : n];
+      *reinterpret_cast<v4u*>(lds + buf * kStage + (wave * kLoads + n) * 1024 + lane * 16) = held[n];
   };
-
-  // LDS offsets of the lane's operand reads: row, chunk 2 step + h
-  uint32_t ra[4];
+  v4f acc[4][4];
 #pragma unroll
-  for (int s = 0; s < 4; ++s) ra[s] = l32 * kRowB + (((2 * s + h) ^ swz(l32)) << 4);
-  const uint32_t wbase = base + wn * TN * 32 * kRowB, xbase = base + (BN + wm * TM * 32) * kRowB;
-
-  v16f acc[TN][TM];
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-  for (int i = 0; i < TN; ++i)
+    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  fetch(s0);
+  put(0);
+  __syncthreads();
+  for (int st = s0; st < s1; ++st) {
+    const int b = (st - s0) & 1;
+    if (st + 1 < s1) fetch(st + 1);
+    const uint8_t* const pw = lds + b * kStage + (wn * 64 + l16) * kRowB;
+    const uint8_t* const px = lds + b * kStage + (B + wm * 64 + l16) * kRowB;
 #pragma unroll
-    for (int j = 0; j < TM; ++j)
+    for (int s = 0; s < 2; ++s) {
+      const int c = ((4 * s + q) ^ (l16 >> 1)) << 4;
+      v4u fw[4], fx[4];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-
-  auto compute = [&](int buf) {
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      v4u fw[TN], fx[TM];
-#pragma unroll
-      for (int i = 0; i < TN; ++i) fw[i] = lds_read16(wbase + buf * kStage + ra[s] + i * 32 * kRowB);
-#pragma unroll
-      for (int j = 0; j < TM; ++j) fx[j] = lds_read16(xbase + buf * kStage + ra[s] + j * 32 * kRowB);
-#pragma unroll
-      for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int j = 0; j < TM; ++j) acc[i][j] = E::mfma(fw[i], fx[j], acc[i][j]);
-    }
-  };
-
-  if constexpr (DMA) {
-    issue(s0, 0);
-    lds_wait_barrier<0>();
-    for (int st = s0; st < s1; ++st) {
-      const int b = (st - s0) & 1;
-      if (st + 1 < s1) issue(st + 1, b ^ 1);
-      compute(b);
-      lds_wait_barrier<0>();
-    }
-  } else {
-    fetch(s0);
-    put(0);
-    __syncthreads();
-    for (int st = s0; st < s1; ++st) {
-      const int b = (st - s0) & 1;
-      if (st + 1 < s1) fetch(st + 1);
-      compute(b);
-      if (st + 1 < s1) put(b ^ 1);
-      __syncthreads();
-    }
-  }
-
-  // Epilogue through the wave's own LDS: 32 rows x 32 TN channels in fp32, 16-byte
-  // chunk c of row r at chunk c ^ (r % (8 TN)), then whole row segments
-  constexpr int kC4 = TN * 8;              // 16-byte chunks of a staged row
-  float* const stage = reinterpret_cast<float*>(lds + wave * 32 * kC4 * 16);
-  constexpr int kLanesRow = TN * 4;        // lanes of a row, 8 channels each
-  const int c8 = lane % kLanesRow;
-  Columns<E> col;
-  const int nl = n0 + wn * TN * 32 + c8 * 8;
-  if (a.splits == 1) col.init(a, nl);
-#pragma unroll
-  for (int j = 0; j < TM; ++j) {
-#pragma unroll
-    for (int i = 0; i < TN; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<v4f*>(stage + (l32 * kC4 + ((i * 8 + 2 * q + h) ^ (l32 & (kC4 - 1)))) * 4) =
-            v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-#pragma unroll 2
-    for (int it = 0; it < 32 * kLanesRow / 64; ++it) {
-      const int r = it * (64 / kLanesRow) + lane / kLanesRow;
-      const v4f lo = *reinterpret_cast<const v4f*>(stage + (r * kC4 + ((2 * c8) ^ (r & (kC4 - 1)))) * 4);
-      const v4f hi = *reinterpret_cast<const v4f*>(stage + (r * kC4 + ((2 * c8 + 1) ^ (r & (kC4 - 1)))) * 4);
-      float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      const int m = m0 + (wm * TM + j) * 32 + r;
-      if (a.splits == 1) {
-        col.finish(a, m, f);
-      } else if (m < a.M && nl < a.N) {
-        float* p = a.part + (static_cast<int64_t>(blockIdx.y) * a.M + m) * a.N + nl;
-        if (nl + 8 <= a.N && (a.N & 3) == 0) {
-          *reinterpret_cast<v4f*>(p) = lo;
-          *reinterpret_cast<v4f*>(p + 4) = hi;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (nl + e < a.N) p[e] = f[e];
-        }
+      for (int i = 0; i < 4; ++i) {
+        fw[i] = *reinterpret_cast<const v4u*>(pw + i * 16 * kRowB + c);
+        fx[i] = *reinterpret_cast<const v4u*>(px + i * 16 * kRowB + c);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = E::mfma16(fw[i], fx[j], acc[i][j]);
     }
+    if (st + 1 < s1) put(b ^ 1);
+    __syncthreads();
   }
+  epilogue<E, B, B, 2, 2, 4, 4, staged_tiles(4, 2 * 16 * B * 4, 2 * kStage)>(a, acc, lds, m0, n0);
 }
 
 // Sum of the splits in their order, then the epilogue: 8 channels a thread.
@@ -381,49 +546,74 @@ __global__ __launch_bounds__(256, 1) void k_linear16_few(LinArgs a) {
   col.finish(a, m, f);
 }
 
-enum { kFew, kMiddle, kLarge };
+// Schedules.  `slots`: workgroups the device holds at once; `light` and
+// `full`: microseconds of a stage of 64 k with one workgroup a CU or fewer
+// and with every slot taken; `fixed`: launch, first loads and epilogue.
+// Measured on bf16 normal values with K from 512 to 12288.
+struct Shape {
+  int bn, bm, slots;
+  float light, full, fixed;
+};
+enum { k256, k128, k128Deep, k64, kAny, kShapes };
+constexpr Shape kShape[kShapes] = {
+    {256, 256, 256, 1.10f, 1.45f, 8.f},   // 8 waves
+    {128, 128, 512, 0.50f, 0.83f, 5.f},   // 4 waves, two workgroups a CU
+    {128, 128, 256, 0.36f, 0.42f, 5.f},   // 8 waves, loads two stages further ahead
+    {64, 64, 512, 0.20f, 0.33f, 4.f},     // 4 waves, one stage further ahead
+    {128, 128, 512, 0.60f, 1.20f, 5.f},   // k_linear16_any
+};
+constexpr int kMaxSplits = 8;
+
 struct Plan {
-  int kind, splits, per;
+  int shape, splits, per;
   size_t bytes;
 };
 
-Plan plan_for(int M, int N, int K) {
-  Plan p{M <= 32 ? kFew : kMiddle, 1, 0, 0};
+// The cheapest shape and number of splits.  Past one round of workgroups
+// the cost lies between the rounded-up and the true number of rounds: idle
+// CUs of the last one leave the others a higher clock.  The join of splits
+// reads and writes them once more.
+Plan plan_for(int M, int N, int K, bool aligned, size_t most) {
   const int stages = (K + 63) / 64;
-  p.per = stages;
-  if (p.kind == kFew) return p;
-  const int64_t big = static_cast<int64_t>((M + 255) / 256) * ((N + 255) / 256);
-  if (big >= 192) {
-    p.kind = kLarge;
-    return p;
-  }
-  const int64_t tiles = static_cast<int64_t>((M + 127) / 128) * ((N + 127) / 128);
-  if (tiles < 256 && stages >= 16) {
-    int64_t s = 512 / tiles;
-    if (s > stages / 8) s = stages / 8;
-    if (s > 16) s = 16;
-    if (s > 1) {
-      p.per = static_cast<int>((stages + s - 1) / s);
-      p.splits = (stages + p.per - 1) / p.per;
-      p.bytes = static_cast<size_t>(p.splits) * M * N * 4;
+  Plan best{kAny, 1, stages, 0};
+  float least = INFINITY;
+  for (int i = aligned ? 0 : kAny; i < (aligned ? kAny : kShapes); ++i) {
+    const Shape& c = kShape[i];
+    const float tiles = static_cast<float>((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+    for (int s = 1; s <= kMaxSplits && s <= stages; ++s) {
+      const int per = (stages + s - 1) / s;
+      if ((stages + per - 1) / per != s) continue;
+      const size_t bytes = s == 1 ? 0 : static_cast<size_t>(s) * M * N * 4;
+      if (bytes > most) break;
+      const float groups = tiles * s, load = groups / c.slots;
+      const float stage = c.light + (c.full - c.light) * fminf(fmaxf(groups - 256.f * (c.slots > 256), 0.f) / 256.f, 1.f);
+      const float rounds = load <= 1.f ? 1.f : 0.5f * (load + ceilf(load));
+      const float us = rounds * per * stage + c.fixed + (s > 1 ? 3.f + bytes * 2e-6f / 4.f : 0.f);
+      if (us < least) {
+        least = us;
+        best = Plan{i, s, per, bytes};
+      }
     }
   }
-  return p;
+  return best;
 }
 
-template <typename E, int B, int WN, int WM, bool DMA>
-void tiles(const LinArgs& a, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((a.M + B - 1) / B) * static_cast<unsigned>((a.N + B - 1) / B), a.splits);
-  k_linear16<E, B, B, WN, WM, DMA><<<grid, WN * WM * 64, 0, stream>>>(a);
+// up to 32 rows the weights are read once by k_linear16_few
+constexpr int kFewRows = 32;
+
+dim3 tiles(const LinArgs& a, int bn, int bm) {
+  return dim3(static_cast<unsigned>((a.M + bm - 1) / bm) * static_cast<unsigned>((a.N + bn - 1) / bn), a.splits);
+}
+
+template <typename E, int BN, int BM, int WN, int WM, int D>
+void start(const LinArgs& a, hipStream_t stream) {
+  k_linear16<E, BN, BM, WN, WM, D><<<tiles(a, BN, BM), WN * WM * 64, 0, stream>>>(a);
 }
 
 template <typename E>
-int launch(LinArgs a, Plan p, hipStream_t stream) {
-  const bool aligned = a.K % 8 == 0 && a.ldx % 8 == 0 && a.ldw % 8 == 0 &&
-                       ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.w)) & 15) == 0;
-  a.splits = p.splits;
-  a.stages_per_split = p.per;
-  if (p.kind == kFew && aligned) {
+int launch(LinArgs a, bool aligned, size_t workspace, hipStream_t stream) {
+  a.splits = 1;
+  if (aligned && a.M <= kFewRows) {
     const unsigned blocks = (a.N + 31) / 32;
     if (a.M <= 4)
       k_linear16_few<E, 1><<<blocks, 256, 0, stream>>>(a);
@@ -433,12 +623,17 @@ int launch(LinArgs a, Plan p, hipStream_t stream) {
       k_linear16_few<E, 4><<<blocks, 256, 0, stream>>>(a);
     else
       k_linear16_few<E, 8><<<blocks, 256, 0, stream>>>(a);
-  } else if (!aligned) {
-    tiles<E, 128, 2, 2, false>(a, stream);
-  } else if (p.kind == kLarge) {
-    tiles<E, 256, 2, 4, true>(a, stream);
-  } else {
-    tiles<E, 128, 2, 2, true>(a, stream);
+    return static_cast<int>(hipGetLastError());
+  }
+  const Plan p = plan_for(a.M, a.N, a.K, aligned, workspace);
+  a.splits = p.splits;
+  a.stages_per_split = p.per;
+  switch (p.shape) {
+    case k256: start<E, 256, 256, 2, 4, 0>(a, stream); break;
+    case k128: start<E, 128, 128, 2, 2, 0>(a, stream); break;
+    case k128Deep: start<E, 128, 128, 2, 4, 2>(a, stream); break;
+    case k64: start<E, 64, 64, 2, 2, 1>(a, stream); break;
+    default: k_linear16_any<E><<<tiles(a, 128, 128), 256, 0, stream>>>(a);
   }
   if (a.splits > 1) {
     const int64_t n = static_cast<int64_t>((a.N + 7) / 8) * a.M;
@@ -451,16 +646,14 @@ int launch(LinArgs a, Plan p, hipStream_t stream) {
 
 extern "C" {
 
-size_t svdq_linear16_plan_bytes(int M, int N, int K) { return plan_for(M, N, K).bytes; }
+size_t svdq_linear16_plan_bytes(int M, int N, int K) {
+  const bool aligned = K % 8 == 0;
+  return aligned && M <= kFewRows ? 0 : plan_for(M, N, K, aligned, SIZE_MAX).bytes;
+}
 
 int svdq_launch_linear16(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const void* gate,
                          int64_t ld_gate, int group_rows, const void* residual, int64_t ldr, void* y, int64_t ldy, int M,
                          int N, int K, int activation, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
-  Plan p = plan_for(M, N, K);
-  if (p.splits > 1 && (!workspace || workspace_bytes < p.bytes)) {
-    p.splits = 1;
-    p.per = (K + 63) / 64;
-  }
   LinArgs a{};
   a.x = static_cast<const uint16_t*>(x);
   a.w = static_cast<const uint16_t*>(w);
@@ -480,7 +673,10 @@ int svdq_launch_linear16(const void* x, int64_t ldx, const void* w, int64_t ldw,
   a.group_rows = group_rows;
   a.act = activation;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  return dtype == SVDQ_BF16 ? launch<Bf16>(a, p, s) : launch<F16>(a, p, s);
+  const bool aligned = K % 8 == 0 && ldx % 8 == 0 && ldw % 8 == 0 &&
+                       ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 15) == 0;
+  const size_t bytes = workspace ? workspace_bytes : 0;
+  return dtype == SVDQ_BF16 ? launch<Bf16>(a, aligned, bytes, s) : launch<F16>(a, aligned, bytes, s);
 }
 
 }  // extern "C"

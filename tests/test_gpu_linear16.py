@@ -78,8 +78,8 @@ def test_large_tiles(m, n, k):
 
 
 def test_split_along_k():
-    for m, n, k in ((100, 256, 4096), (40, 130, 2048 + 8), (300, 33, 1024)):
-        assert bq.linear16_workspace_size(m, n, k) > 0
+    for m, n, k, split in ((100, 256, 4096, True), (40, 130, 2048 + 8, True), (300, 33, 1024, False)):
+        assert (bq.linear16_workspace_size(m, n, k) > 0) == split
         a = check(m, n, k, act="gelu", residual=True, gate=2)
         b = check(m, n, k, act="gelu", residual=True, gate=2, workspace=None)
         assert torch.equal(a, check(m, n, k, act="gelu", residual=True, gate=2))
