@@ -179,7 +179,7 @@ struct WaveTile {
 #pragma unroll
     for (int st = 0; st < kSteps; ++st)
 #pragma unroll
-      for (int kt = 0; kt < kKt; ++kt) s[kt] = E::mfma(lds_read16(kbuf + ka[st] + kt * 32 * DP * 2), qf[st], s[kt]);
+      for (int kt = 0; kt < kKt; ++kt) s[kt] = E::mfma(read_k(kbuf, kt, st), qf[st], s[kt]);
   }
 
   // keys key0 + .. at or past lim are out of the row's sight
@@ -191,23 +191,35 @@ struct WaveTile {
       for (int e = 0; e < 16; ++e) s[kt][e] = kt * 32 + (e >> 2) * 8 + (e & 3) < left ? s[kt][e] : -INFINITY;
   }
 
-  // the row's maximum against the reference; O and l move to a new
-  // reference if any row of the wave needs it
-  __device__ __forceinline__ void raise(const v16f (&s)[kKt]) {
+  __device__ __forceinline__ v4u read_k(uint32_t kbuf, int kt, int st) const { return lds_read16(kbuf + ka[st] + kt * 32 * DP * 2); }
+  // 16 keys of V^T: 4 + 4 of them for each lane half
+  __device__ __forceinline__ v4u read_v(uint32_t vbuf, int ks, int d) const {
+    const v2u lo = lds_read_tr(vbuf + va[d] + ks * 16 * DP * 2);
+    const v2u hi = lds_read_tr(vbuf + va[d] + (ks * 16 + 8) * DP * 2);
+    return v4u{lo.x, lo.y, hi.x, hi.y};
+  }
+
+  // maximum over the two lanes that hold a row's keys
+  static __device__ __forceinline__ float pair_max(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __builtin_elementwise_maximum(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  __device__ __forceinline__ float top(const v16f (&s)[kKt]) const {
     float mx = s[0][0];
 #pragma unroll
     for (int kt = 0; kt < kKt; ++kt)
 #pragma unroll
       for (int e = 0; e < 16; ++e) mx = __builtin_elementwise_maximum(mx, s[kt][e]);
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
-    mx = __builtin_elementwise_maximum(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    return pair_max(mx);
+  }
+  // the row's maximum against the reference; O and l move to a new one if
+  // any row of the wave needs it
+  __device__ __forceinline__ void raise(float mx) {
     if (__ballot(mx > limit)) {
       const float m_new = mx > m ? mx : m;
       const float f = m == -INFINITY ? 0.f : exp2_fast((m - m_new) * sc);
 #pragma unroll
-      for (int d = 0; d < kDt; ++d)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[d][e] *= f;
+      for (int d = 0; d < kDt; ++d) acc[d] *= f;
       l *= f;
       m = m_new;
       limit = m + slack;
@@ -215,19 +227,20 @@ struct WaveTile {
     }
   }
 
-  __device__ __forceinline__ void weights(v16f (&s)[kKt], v4u (&p)[2 * kKt]) {
-    float part[4] = {0.f, 0.f, 0.f, 0.f};
+  // pair i of the lane's 8 kKt pairs of weights
+  __device__ __forceinline__ void weigh(const v16f (&s)[kKt], v4u (&p)[2 * kKt], int i, float& sum) const {
+    const int kt = i >> 3, e = (i & 7) * 2;
+    const float x = exp2_fast(__builtin_fmaf(s[kt][e], sc, -msc));
+    const float y = exp2_fast(__builtin_fmaf(s[kt][e + 1], sc, -msc));
+    sum += x;
+    sum += y;
+    p[i >> 2][i & 3] = E::pack2(x, y);
+  }
+  __device__ __forceinline__ void weights(const v16f (&s)[kKt], v4u (&p)[2 * kKt]) {
+    float sum = 0.f;
 #pragma unroll
-    for (int kt = 0; kt < kKt; ++kt)
-#pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        const float a = exp2_fast(__builtin_fmaf(s[kt][e], sc, -msc));
-        const float b = exp2_fast(__builtin_fmaf(s[kt][e + 1], sc, -msc));
-        part[(e >> 1) & 1] += a;
-        part[2 + ((e >> 1) & 1)] += b;
-        p[2 * kt + (e >> 3)][(e >> 1) & 3] = E::pack2(a, b);
-      }
-    l += (part[0] + part[1]) + (part[2] + part[3]);
+    for (int i = 0; i < 8 * kKt; ++i) weigh(s, p, i, sum);
+    l += sum;
   }
 
   __device__ __forceinline__ void accumulate(uint32_t vbuf, const v4u (&p)[2 * kKt]) {
@@ -235,9 +248,7 @@ struct WaveTile {
     for (int ks = 0; ks < 2 * kKt; ++ks)
 #pragma unroll
       for (int d = 0; d < kDt; ++d) {
-        const v2u lo = lds_read_tr(vbuf + va[d] + ks * 16 * DP * 2);
-        const v2u hi = lds_read_tr(vbuf + va[d] + (ks * 16 + 8) * DP * 2);
-        acc[d] = E::mfma(v4u{lo.x, lo.y, hi.x, hi.y}, p[ks], acc[d]);
+        acc[d] = E::mfma(read_v(vbuf, ks, d), p[ks], acc[d]);
       }
   }
 
@@ -273,10 +284,17 @@ __device__ __forceinline__ Job job_of(const AttnArgs& a, int id) {
 // ---------------------------------------------------------------------------
 // Many rows: NW waves of 32 rows share tiles of 64 keys.
 //
-// K runs one tile ahead of V: iteration i multiplies Q with K tile i + 1
-// while the softmax of tile i runs on the vector units, so that matrix and
-// vector work of one wave overlap, and two waves share a SIMD.  Tiles come
-// straight to LDS, double-buffered, with one barrier an iteration.
+// Iteration i has two phases, in each of which matrix and vector work stand
+// side by side in the instruction order (a wave issues in order; two waves
+// share a SIMD):
+//   A  S of tile i + 1 (K), beside most weights of tile i
+//   B  O += P V of tile i, beside the last weights of tile i and the maxima
+//      of tile i + 1
+// Operands are read from LDS kAhead products ahead, K's first ones of the
+// next iteration before its barrier.  Tiles come straight to LDS, two
+// iterations ahead: K of tile i + 4 and V of tile i + 2, through four and
+// three slots, with one barrier an iteration.  Products of 32 x 32 x 16: the
+// vector work needs the issue slots that twice as many of 16 x 16 x 32 take.
 // ---------------------------------------------------------------------------
 
 template <typename E, int DP, int NW>
@@ -285,8 +303,9 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
   using W = WaveTile<E, DP, kKeys>;
   constexpr int kBuf = W::kBytes;
   constexpr int kLoads = kBuf / 1024 / NW;   // 1 KB loads per wave and operand tile
-  static_assert(kLoads >= 1 && NW * 32 * DP * 2 <= 4 * kBuf, "loads divide evenly; the output staging fits");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kBuf];   // K0 K1 V0 V1
+  constexpr int kSlotsK = 4, kSlotsV = 3;
+  static_assert(kLoads >= 1 && NW * 32 * DP * 2 <= (kSlotsK + kSlotsV) * kBuf, "loads divide evenly; the output staging fits");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[(kSlotsK + kSlotsV) * kBuf];
 
   const Job job = job_of(a, blockIdx.x);
   const Tile t = find_tile<BM>(a, job.slot);
@@ -325,49 +344,143 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
   const uint32_t dst = base + wave * kLoads * 1024;
   const uint16_t* const kp = a.k + t.k0 * a.k_t + job.head * a.k_h;
   const uint16_t* const vp = a.v + t.k0 * a.v_t + job.head * a.v_h;
-  auto load_k = [&](int i, int buf) {
-    const int left = t.len_k - i * kKeys;
-    const auto r = buffer_of(kp + i * kKeys * a.k_t, (left - 1) * a.k_t * 2 + a.D * 2);
-#pragma unroll
-    for (int n = 0; n < kLoads; ++n) dma_b128(r, dst + buf * kBuf + n * 1024, kv[n]);
+  // Tile i of K or V: its rows that exist, none past this split.  Loads are
+  // made for every tile, those of none bring zeros without going to memory:
+  // no branch parts the products from the vector work beside them.
+  auto tile = [&](const uint16_t* p, int64_t stride, int i) {
+    const int rows = i < t1 ? min(t.len_k - i * kKeys, kKeys) : 0;
+    return buffer_of(p + i * (kKeys * stride), rows > 0 ? (rows - 1) * static_cast<int>(stride) * 2 + a.D * 2 : 0);
   };
-  auto load_v = [&](int i, int buf) {
-    const int left = t.len_k - i * kKeys;
-    const auto r = buffer_of(vp + i * kKeys * a.v_t, (left - 1) * a.v_t * 2 + a.D * 2);
-#pragma unroll
-    for (int n = 0; n < kLoads; ++n) dma_b128(r, dst + (2 + buf) * kBuf + n * 1024, vv[n]);
-  };
+  constexpr uint32_t kV = kSlotsK * kBuf;
+  constexpr int kProducts = W::kKt * W::kSteps;         // of phase A, and of phase B
+  constexpr int kAhead = 4, kWeights = 8 * W::kKt;      // pairs of weights
+  constexpr int kLate = 4;                              // of which in phase B: those of the last 16 keys
+  static_assert(kProducts == 2 * W::kKt * W::kDt && 4 * kLoads <= kProducts, "work divides evenly over the products");
 
-  v16f s[W::kKt];
   if (t0 < t1) {
-    load_k(t0, 0);
-    load_v(t0, 0);
-    if (t0 + 1 < t1) load_k(t0 + 1, 1);
-    lds_wait_barrier<0>();
-    w.scores(base, s);
-    lds_wait_barrier<0>();
-
-    auto iterate = [&](int i, auto masked, auto next) {
-      const int b = (i - t0) & 1;
-      if (i + 2 < t1) load_k(i + 2, b);
-      if (i + 1 < t1) load_v(i + 1, b ^ 1);
-      if constexpr (decltype(masked)::value) w.mask(s, i * kKeys, lim, h);
-      w.raise(s);
-      v4u p[2 * W::kKt];
-      v16f s_next[W::kKt];
-      if constexpr (decltype(next)::value) w.scores(base + (b ^ 1) * kBuf, s_next);
-      w.weights(s, p);
-      w.accumulate(base + (2 + b) * kBuf, p);
-      lds_wait_barrier<0>();
-      if constexpr (decltype(next)::value) {
+    auto load = [&](const uint16_t* p, int64_t stride, int i, const int (&v)[kLoads], uint32_t slot) {
+      const auto r = tile(p, stride, i);
 #pragma unroll
-        for (int kt = 0; kt < W::kKt; ++kt) s[kt] = s_next[kt];
+      for (int n = 0; n < kLoads; ++n) dma_b128(r, dst + slot + n * 1024, v[n]);
+    };
+    load(kp, a.k_t, t0, kv, 0);
+    load(kp, a.k_t, t0 + 1, kv, kBuf);
+    load(vp, a.v_t, t0, vv, kV);
+    load(kp, a.k_t, t0 + 2, kv, 2 * kBuf);
+    load(vp, a.v_t, t0 + 1, vv, kV + kBuf);
+    load(kp, a.k_t, t0 + 3, kv, 3 * kBuf);
+    lds_wait_barrier<4 * kLoads>();   // K of the first two tiles
+    v16f s0[W::kKt], s1[W::kKt];
+    w.scores(base, s0);
+    if (t0 >= open) w.mask(s0, t0 * kKeys, lim, h);
+    float mx = w.top(s0);
+    v4u f[kAhead];   // operands read ahead
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) f[j] = w.read_k(base + kBuf, j % W::kKt, j / W::kKt);
+    lds_wait_barrier<2 * kLoads>();   // V of the first tile, K of the third
+    // slots of K's tiles i (free), i + 1, and of V's tile i
+    uint32_t k0 = 0, v0 = kV;
+    auto after_k = [](uint32_t u, int n) { return u + n * kBuf < kSlotsK * kBuf ? u + n * kBuf : u + n * kBuf - kSlotsK * kBuf; };
+    auto after_v = [](uint32_t u, int n) {
+      return u + n * kBuf < kV + kSlotsV * kBuf ? u + n * kBuf : u + n * kBuf - kSlotsV * kBuf;
+    };
+
+    // tile i's scores in s; those of tile i + 1 go to s_next
+    auto iterate = [&](int i, v16f (&s)[W::kKt], v16f (&s_next)[W::kKt], auto masked, auto next) {
+      constexpr bool kNext = decltype(next)::value;
+      const uint32_t k1 = after_k(k0, 1), k2 = after_k(k0, 2), v1 = after_v(v0, 1), v2 = after_v(v0, 2);
+      const auto rk = tile(kp, a.k_t, i + 4), rv = tile(vp, a.v_t, i + 2);
+      w.raise(mx);
+      v4u p[2 * W::kKt];
+      float sum[2] = {0.f, 0.f};
+      // pairs of weights that go beside product j of n
+      auto weigh = [&](int first, int count, int j, int n) {
+#pragma unroll
+        for (int x = first + j * count / n; x < first + (j + 1) * count / n; ++x) w.weigh(s, p, x, sum[x & 1]);
+      };
+#pragma unroll
+      for (int j = 0; j < kProducts; ++j) {
+        const int st = j / W::kKt, kt = j % W::kKt;
+        if constexpr (kNext) {
+          if (st == 0)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s_next[kt][e] = 0.f;
+          s_next[kt] = E::mfma(f[j % kAhead], w.qf[st], s_next[kt]);
+        }
+        // the next operand: K's, then V's first ones
+        if (j + kAhead < kProducts) {
+          if constexpr (kNext) f[j % kAhead] = w.read_k(base + k1, (j + kAhead) % W::kKt, (j + kAhead) / W::kKt);
+        } else {
+          const int n = j + kAhead - kProducts;
+          f[j % kAhead] = w.read_v(base + v0, n / W::kDt, n % W::kDt);
+        }
+        weigh(0, kWeights - kLate, j, kProducts);
+        // tiles i + 2 of V and i + 4 of K, early and apart
+        if constexpr (kNext)
+          if (j % 2 == 0 && j / 2 < 2 * kLoads) {
+            if (j / 2 < kLoads)
+              dma_b128(rv, dst + v2 + j / 2 * 1024, vv[j / 2]);
+            else
+              dma_b128(rk, dst + k0 + (j / 2 - kLoads) * 1024, kv[j / 2 - kLoads]);
+          }
+        fence();
+      }
+      if constexpr (kNext && decltype(masked)::value) w.mask(s_next, (i + 1) * kKeys, lim, h);
+      if constexpr (kNext) mx = s_next[0][0];
+      order();
+#pragma unroll
+      for (int j = 0; j < kProducts; ++j) {
+        const int ks = j / W::kDt, d = j % W::kDt;
+        w.acc[d] = E::mfma(f[j % kAhead], p[ks], w.acc[d]);
+        if (j + kAhead < kProducts) {
+          const int n = j + kAhead;
+          f[j % kAhead] = w.read_v(base + v0, n / W::kDt, n % W::kDt);
+        } else if constexpr (kNext) {   // past the last tile: a slot's old bytes, not used
+          const int n = j + kAhead - kProducts;
+          f[j % kAhead] = w.read_k(base + k2, n % W::kKt, n / W::kKt);
+        }
+        // the last weights before the products that take them, then the maxima
+        constexpr int kHalf = kProducts / 2;
+        if (j < kHalf) weigh(kWeights - kLate, kLate, j, kHalf);
+        if constexpr (kNext) {
+          if (j >= kHalf) {
+            constexpr int kE = 16 * W::kKt / kHalf;
+#pragma unroll
+            for (int x = 0; x < kE; ++x) {
+              const int n = (j - kHalf) * kE + x;
+              mx = __builtin_elementwise_maximum(mx, s_next[n / 16][n % 16]);
+            }
+          }
+        }
+        fence();
+      }
+      w.l += sum[0] + sum[1];
+      if constexpr (kNext) {
+        mx = W::pair_max(mx);
+        // this tile is read out (all but K's operands read ahead are back);
+        // K of tile i + 3 and V of tile i + 1 have landed
+        order();
+        lds_wait_barrier<2 * kLoads, kAhead>();
+        k0 = k1;
+        v0 = v1;
+      } else {
+        lds_wait_barrier<0>();
       }
     };
+    using Yes = std::true_type;
+    using No = std::false_type;
     int i = t0;
-    for (; i < min(open, t1 - 1); ++i) iterate(i, std::false_type{}, std::true_type{});
-    for (; i < t1 - 1; ++i) iterate(i, std::true_type{}, std::true_type{});
-    iterate(i, std::true_type{}, std::false_type{});
+    const int plain = min(open, t1) - 1;   // iterations whose next tile needs no mask
+    for (; i + 1 < plain; i += 2) {
+      iterate(i, s0, s1, No{}, Yes{});
+      iterate(i + 1, s1, s0, No{}, Yes{});
+    }
+    for (; i < t1 - 1; ++i) {
+      iterate(i, s0, s1, Yes{}, Yes{});
+#pragma unroll
+      for (int kt = 0; kt < W::kKt; ++kt) s0[kt] = s1[kt];
+    }
+    iterate(i, s0, s1, No{}, No{});
   }
 
   const float l = w.row_sum();
@@ -481,7 +594,7 @@ __global__ __launch_bounds__(256, 1) void k_attention_few(AttnArgs a) {
     v16f s[1];
     w.scores(base + 2 * b * kBuf, s);
     if ((i + 1) * kKeys > first_lim) w.mask(s, i * kKeys, lim, h);
-    w.raise(s);
+    w.raise(w.top(s));
     v4u p[2];
     w.weights(s, p);
     w.accumulate(base + (2 * b + 1) * kBuf, p);
