@@ -291,9 +291,9 @@ __device__ __forceinline__ Job job_of(const AttnArgs& a, int id) {
 //   B  O += P V of tile i, beside the last weights of tile i and the maxima
 //      of tile i + 1
 // Operands are read from LDS kAhead products ahead, K's first ones of the
-// next iteration before its barrier.  Tiles come straight to LDS, two
-// iterations ahead: K of tile i + 4 and V of tile i + 2, through four and
-// three slots, with one barrier an iteration.  Products of 32 x 32 x 16: the
+// next iteration before its barrier.  Tiles come straight to LDS, kLead
+// iterations ahead: K of tile i + 2 + kLead and V of tile i + kLead, through
+// rings of slots, with one barrier an iteration.  Products of 32 x 32 x 16: the
 // vector work needs the issue slots that twice as many of 16 x 16 x 32 take.
 // ---------------------------------------------------------------------------
 
@@ -303,7 +303,8 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
   using W = WaveTile<E, DP, kKeys>;
   constexpr int kBuf = W::kBytes;
   constexpr int kLoads = kBuf / 1024 / NW;   // 1 KB loads per wave and operand tile
-  constexpr int kSlotsK = 4, kSlotsV = 3;
+  // tiles ahead of the ones in use; with 4 waves two workgroups share a CU's LDS
+  constexpr int kLead = NW == 8 ? 2 : 1, kSlotsK = 2 + kLead, kSlotsV = 1 + kLead;
   static_assert(kLoads >= 1 && NW * 32 * DP * 2 <= (kSlotsK + kSlotsV) * kBuf, "loads divide evenly; the output staging fits");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[(kSlotsK + kSlotsV) * kBuf];
 
@@ -363,13 +364,16 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
 #pragma unroll
       for (int n = 0; n < kLoads; ++n) dma_b128(r, dst + slot + n * 1024, v[n]);
     };
+    // K0 K1 V0, then what is further ahead: K2 (V1 K3)
     load(kp, a.k_t, t0, kv, 0);
     load(kp, a.k_t, t0 + 1, kv, kBuf);
     load(vp, a.v_t, t0, vv, kV);
     load(kp, a.k_t, t0 + 2, kv, 2 * kBuf);
-    load(vp, a.v_t, t0 + 1, vv, kV + kBuf);
-    load(kp, a.k_t, t0 + 3, kv, 3 * kBuf);
-    lds_wait_barrier<4 * kLoads>();   // K of the first two tiles
+    if constexpr (kLead == 2) {
+      load(vp, a.v_t, t0 + 1, vv, kV + kBuf);
+      load(kp, a.k_t, t0 + 3, kv, 3 * kBuf);
+    }
+    lds_wait_barrier<2 * kLead * kLoads>();   // K of the first two tiles
     v16f s0[W::kKt], s1[W::kKt];
     w.scores(base, s0);
     if (t0 >= open) w.mask(s0, t0 * kKeys, lim, h);
@@ -377,7 +381,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
     v4u f[kAhead];   // operands read ahead
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) f[j] = w.read_k(base + kBuf, j % W::kKt, j / W::kKt);
-    lds_wait_barrier<2 * kLoads>();   // V of the first tile, K of the third
+    lds_wait_barrier<2 * (kLead - 1) * kLoads>();   // V of the first tile, K of the third
     // slots of K's tiles i (free), i + 1, and of V's tile i
     uint32_t k0 = 0, v0 = kV;
     auto after_k = [](uint32_t u, int n) { return u + n * kBuf < kSlotsK * kBuf ? u + n * kBuf : u + n * kBuf - kSlotsK * kBuf; };
@@ -388,8 +392,8 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
     // tile i's scores in s; those of tile i + 1 go to s_next
     auto iterate = [&](int i, v16f (&s)[W::kKt], v16f (&s_next)[W::kKt], auto masked, auto next) {
       constexpr bool kNext = decltype(next)::value;
-      const uint32_t k1 = after_k(k0, 1), k2 = after_k(k0, 2), v1 = after_v(v0, 1), v2 = after_v(v0, 2);
-      const auto rk = tile(kp, a.k_t, i + 4), rv = tile(vp, a.v_t, i + 2);
+      const uint32_t k1 = after_k(k0, 1), k2 = after_k(k0, 2), v1 = after_v(v0, 1), vl = after_v(v0, kLead);
+      const auto rk = tile(kp, a.k_t, i + 2 + kLead), rv = tile(vp, a.v_t, i + kLead);
       w.raise(mx);
       v4u p[2 * W::kKt];
       float sum[2] = {0.f, 0.f};
@@ -415,11 +419,11 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
           f[j % kAhead] = w.read_v(base + v0, n / W::kDt, n % W::kDt);
         }
         weigh(0, kWeights - kLate, j, kProducts);
-        // tiles i + 2 of V and i + 4 of K, early and apart
+        // the loads of the tiles ahead, early and apart
         if constexpr (kNext)
           if (j % 2 == 0 && j / 2 < 2 * kLoads) {
             if (j / 2 < kLoads)
-              dma_b128(rv, dst + v2 + j / 2 * 1024, vv[j / 2]);
+              dma_b128(rv, dst + vl + j / 2 * 1024, vv[j / 2]);
             else
               dma_b128(rk, dst + k0 + (j / 2 - kLoads) * 1024, kv[j / 2 - kLoads]);
           }
@@ -460,7 +464,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
         // this tile is read out (all but K's operands read ahead are back);
         // K of tile i + 3 and V of tile i + 1 have landed
         order();
-        lds_wait_barrier<2 * kLoads, kAhead>();
+        lds_wait_barrier<2 * (kLead - 1) * kLoads, kAhead>();
         k0 = k1;
         v0 = v1;
       } else {
@@ -625,8 +629,9 @@ __global__ __launch_bounds__(256, 1) void k_attention_few(AttnArgs a) {
           v4f{w.acc[d][4 * j] * f, w.acc[d][4 * j + 1] * f, w.acc[d][4 * j + 2] * f, w.acc[d][4 * j + 3] * f};
   if (h == 0) lds_l[wave][l32] = l * f;
   __syncthreads();
-  // thread: row threadIdx.x / 8, every eighth 4 columns
-  const int r = threadIdx.x >> 3;
+  // kOf threads a row, each every kOf-th 4 columns
+  constexpr int kOf = 2 * NW;
+  const int r = threadIdx.x / kOf;
   const int rr = t.row0 + r;
   if (rr >= t.rows) return;
   float m_row = lds_m[0][r], l_row = lds_l[0][r];
@@ -640,14 +645,14 @@ __global__ __launch_bounds__(256, 1) void k_attention_few(AttnArgs a) {
   const int64_t out_row = static_cast<int64_t>(t.q0 + tok) * a.heads_q + hd;
   const int64_t part = static_cast<int64_t>(job.split) * a.total_q * a.heads_q + out_row;
   const bool whole = a.splits == 1;
-  if ((threadIdx.x & 7) == 0) {
+  if (threadIdx.x % kOf == 0) {
     if (!whole)
       a.part_ml[part] = make_float2(m_row, l_row);
     else if (a.lse)
       a.lse[out_row] = lse_of(m_row, l_row, a.scale);
   }
   const float inv = l_row == 0.f ? 0.f : 1.f / l_row;
-  for (int d = (threadIdx.x & 7) * 4; d < a.D; d += 32) {
+  for (int d = threadIdx.x % kOf * 4; d < a.D; d += kOf * 4) {
     v4f x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NW; ++i) x += *reinterpret_cast<const v4f*>(reinterpret_cast<float*>(lds + i * 4 * kBuf) + r * kRow + d);
@@ -704,15 +709,15 @@ struct Plan {
 
 // The schedule from the sizes the host knows.  Lengths are on the device, so
 // the mean stands for them; every schedule is right for any lengths.
-Plan plan_for(int total_q, int total_k, int batch, int heads_q, int heads_k, int D) {
+Plan plan_for(int total_q, int total_k, int batch, int heads_q, int heads_k, int D, bool causal) {
   const int64_t rows = static_cast<int64_t>(total_q) * (heads_q / heads_k);
   const int64_t mean_rows = rows / batch, mean_keys = total_k / batch;
+  auto units = [&](int bm) { return (rows / bm > batch ? rows / bm : batch) * heads_k; };
   Plan p;
-  p.waves = mean_rows <= 64 ? 0 : 8;
-  const int bm = p.waves ? p.waves * 32 : 32;
-  const int64_t units = (rows / bm > batch ? rows / bm : batch) * heads_k;
+  p.waves = mean_rows <= 64 ? 0 : causal || units(256) < 256 ? 4 : 8;
+  const int64_t n = units(p.waves ? p.waves * 32 : 32);
   const int64_t want = p.waves ? 256 : 1024, keys = p.waves ? 512 : 256;
-  int64_t s = units >= want / 2 ? 1 : (want + units - 1) / units;
+  int64_t s = n >= want / 2 ? 1 : (want + n - 1) / n;
   if (s > mean_keys / keys) s = mean_keys / keys;
   p.splits = static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
   p.bytes = p.splits == 1 ? 0 : static_cast<size_t>(p.splits) * total_q * heads_q * (D + 2) * 4;
@@ -731,6 +736,11 @@ int launch(AttnArgs a, const Plan& p, hipStream_t stream) {
       k_attention<E, 128, 8><<<grid, 512, 0, stream>>>(a);
     else
       k_attention<E, 64, 8><<<grid, 512, 0, stream>>>(a);
+  } else if (p.waves == 4) {
+    if (wide)
+      k_attention<E, 128, 4><<<grid, 256, 0, stream>>>(a);
+    else
+      k_attention<E, 64, 4><<<grid, 256, 0, stream>>>(a);
   } else {
     if (wide)
       k_attention_few<E, 128><<<grid, 256, 0, stream>>>(a);
@@ -749,14 +759,16 @@ int launch(AttnArgs a, const Plan& p, hipStream_t stream) {
 extern "C" {
 
 size_t svdq_attention_plan_bytes(int total_q, int total_k, int batch, int heads_q, int heads_k, int head_dim) {
-  return plan_for(total_q, total_k, batch, heads_q, heads_k, head_dim).bytes;
+  const size_t full = plan_for(total_q, total_k, batch, heads_q, heads_k, head_dim, false).bytes;
+  const size_t causal = plan_for(total_q, total_k, batch, heads_q, heads_k, head_dim, true).bytes;
+  return full > causal ? full : causal;
 }
 
 int svdq_launch_attention(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_q,
                           const int32_t* cu_k, int batch, int total_q, int total_k, int heads_q, int heads_k,
                           int head_dim, const int64_t* strides, float scale, int causal, int dtype, void* workspace,
                           size_t workspace_bytes, void* stream) {
-  Plan p = plan_for(total_q, total_k, batch, heads_q, heads_k, head_dim);
+  Plan p = plan_for(total_q, total_k, batch, heads_q, heads_k, head_dim, causal);
   if (!workspace || workspace_bytes < p.bytes) p.splits = 1;
   AttnArgs a{};
   a.q = static_cast<const uint16_t*>(q);
