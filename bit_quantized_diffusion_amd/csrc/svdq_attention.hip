@@ -525,7 +525,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
     const int tok = rr / a.group;
     const v4u x = *reinterpret_cast<const v4u*>(stage + r * DP * 2 + ((c ^ swz_k<DP>(r)) << 4));
     if (rr < t.rows && c * 8 < a.D)
-      *reinterpret_cast<v4u*>(a.o + (t.q0 + tok) * a.o_t + (job.head * a.group + rr - tok * a.group) * a.o_h + c * 8) = x;
+      stream8(a.o + (t.q0 + tok) * a.o_t + (job.head * a.group + rr - tok * a.group) * a.o_h + c * 8, x);
   }
 }
 
@@ -714,7 +714,15 @@ Plan plan_for(int total_q, int total_k, int batch, int heads_q, int heads_k, int
   const int64_t mean_rows = rows / batch, mean_keys = total_k / batch;
   auto units = [&](int bm) { return (rows / bm > batch ? rows / bm : batch) * heads_k; };
   Plan p;
-  p.waves = mean_rows <= 64 ? 0 : causal || units(256) < 256 ? 4 : 8;
+  // Rows by the 32 (k_attention_few): single tokens, and small grids of short
+  // sequences that fit one round (256 tokens x 24 heads 9.2 -> 7.8 us; with
+  // more workgroups than CUs 128-row tiles win, 512 tokens 31 against 14 us).
+  // Tiles of 128 rows: causal (4608 x 24 heads 166 -> 147 us), grids that 256
+  // rows would not fill, and few keys, where starting up is most of it (8192
+  // rows x 10 heads over 77 and 154 keys 16 -> 13 us).  Else 256 rows, which
+  // read the keys half as often (4608 x 24 heads 270 -> 255 us).
+  const bool few = mean_rows <= 64 || (mean_rows <= 256 && units(32) <= 256);
+  p.waves = few ? 0 : causal || units(256) < 256 || mean_keys < 1024 ? 4 : 8;
   const int64_t n = units(p.waves ? p.waves * 32 : 32);
   const int64_t want = p.waves ? 256 : 1024, keys = p.waves ? 512 : 256;
   int64_t s = n >= want / 2 ? 1 : (want + n - 1) / n;

@@ -164,6 +164,12 @@ __device__ __forceinline__ void store8(uint16_t* p, v4u v, int count) {
   for (int e = 0; e < 7; ++e)
     if (e < count) p[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
 }
+// the same, not kept in the caches on its way (results that the kernel does
+// not read again)
+__device__ __forceinline__ void stream8(uint16_t* p, v4u v) {
+  typedef unsigned v4u_any __attribute__((ext_vector_type(4), aligned(2)));
+  __builtin_nontemporal_store(v, reinterpret_cast<v4u_any*>(p));
+}
 template <typename E>
 __device__ __forceinline__ void unpack8(v4u v, float (&f)[8]) {
 #pragma unroll

@@ -165,7 +165,8 @@ __device__ __forceinline__ void epilogue(const LinArgs& a, const v4f (&acc)[TN][
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] += x[e];
         }
-        store8(a.y + (m0 + tile_row(jp, r)) * a.ldy + nl, pack8<E>(f), 8);
+        // streamed past the caches, which keep the operands (4608 x 3072 x 3072 with gate and residual: 81 -> 71 us)
+        stream8(a.y + (m0 + tile_row(jp, r)) * a.ldy + nl, pack8<E>(f));
       }
     } else {
 #pragma unroll 1

@@ -132,7 +132,11 @@ __global__ __launch_bounds__(WAVES > 1 ? WAVES * 64 : 256) void k_layer_norm(Nor
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[c][e] += w[e];
     }
-    store8(y + k, pack8<E>(f[c]), TAIL ? a.K - k : 8);
+    // streamed: y is not read again here (4608 x 3072: 15 -> 12 us)
+    if (!TAIL || k + 8 <= a.K)
+      stream8(y + k, pack8<E>(f[c]));
+    else
+      store8(y + k, pack8<E>(f[c]), a.K - k);
   }
 }
 
