@@ -50,6 +50,12 @@ struct AttnArgs {
   int total_q, total_k, batch, heads_q, heads_k, group, D;
   float scale;           // > 0
   int causal, splits, slots;
+  // k_attention_spread: workgroups, results of their pieces, and the pieces
+  // of the sequences before each (keys x rows in tiles of 32, and rows alone)
+  int spread;
+  int64_t results;       // that the workspace holds
+  int64_t* before;       // [batch + 1]
+  int32_t* before_q;     // [batch + 1]
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -61,47 +67,53 @@ struct Tile {
   bool any;
 };
 
-// Rows are cut into tiles of BM per sequence.  Sequence i owns the slots
-// from floor(cu[i] g / BM) + i up to the next sequence's first: at least as
-// many as it has tiles, and known without reading lengths on the host.  The
-// slots left over exit.  The owner of a slot is found by a 64-way search.
-template <int BM>
-__device__ __forceinline__ Tile find_tile(const AttnArgs& a, int slot) {
-  int seq = 0;
-  if (a.batch > 1) {
-    const int lane = threadIdx.x & 63;
-    int n = a.batch;
-    while (n > 1) {
-      const int step = (n + 63) >> 6;
-      const int i = seq + lane * step;
-      bool before = false;
-      if (lane * step < n) {
-        const int64_t rows = static_cast<int64_t>(min(max(a.cu_q[i], 0), a.total_q)) * a.group;
-        before = rows / BM + i <= slot;
-      }
-      const int c = max(static_cast<int>(__popcll(__ballot(before))), 1);
-      const int next = seq + (c - 1) * step;
-      n = min(step, n - (c - 1) * step);
-      seq = next;
-    }
-    seq = __builtin_amdgcn_readfirstlane(seq);
+// The last i in [0, n) with before(i), for a condition that holds up to some
+// i (i = 0 at least): a 64-way search by the wave.
+template <typename F>
+__device__ __forceinline__ int last_before(int n, F before) {
+  const int lane = threadIdx.x & 63;
+  int at = 0;
+  while (n > 1) {
+    const int step = (n + 63) >> 6;
+    const bool b = lane * step < n && before(at + lane * step);
+    const int c = max(static_cast<int>(__popcll(__ballot(b))), 1);
+    at += (c - 1) * step;
+    n = min(step, n - (c - 1) * step);
   }
+  return __builtin_amdgcn_readfirstlane(at);
+}
+
+// Sequence seq's tokens, inside the tensors whatever the starts hold.
+__device__ __forceinline__ Tile sequence(const AttnArgs& a, int seq) {
   Tile t;
-  t.q0 = 0;
+  t.q0 = t.k0 = 0;
   t.len_q = a.total_q;
-  int64_t first = 0;
+  t.len_k = a.total_k;
   if (a.cu_q) {
     t.q0 = min(max(a.cu_q[seq], 0), a.total_q);
     t.len_q = min(max(a.cu_q[seq + 1], t.q0), a.total_q) - t.q0;
-    first = static_cast<int64_t>(t.q0) * a.group / BM + seq;
-  }
-  t.k0 = 0;
-  t.len_k = a.total_k;
-  if (a.cu_k) {
     t.k0 = min(max(a.cu_k[seq], 0), a.total_k);
     t.len_k = min(max(a.cu_k[seq + 1], t.k0), a.total_k) - t.k0;
   }
   t.rows = t.len_q * a.group;
+  t.row0 = 0;
+  t.any = t.rows > 0;
+  return t;
+}
+
+// Rows are cut into tiles of BM per sequence.  Sequence i owns the slots
+// from floor(cu[i] g / BM) + i up to the next sequence's first: at least as
+// many as it has tiles, and known without reading lengths on the host.  The
+// slots left over exit.
+template <int BM>
+__device__ __forceinline__ Tile find_tile(const AttnArgs& a, int slot) {
+  int seq = 0;
+  if (a.batch > 1)
+    seq = last_before(a.batch, [&](int i) {
+      return static_cast<int64_t>(min(max(a.cu_q[i], 0), a.total_q)) * a.group / BM + i <= slot;
+    });
+  Tile t = sequence(a, seq);
+  const int64_t first = static_cast<int64_t>(t.q0) * a.group / BM + seq;
   const int64_t row0 = (slot - first) * BM;
   t.any = slot >= first && row0 < t.rows;
   t.row0 = t.any ? static_cast<int>(row0) : 0;
@@ -530,138 +542,302 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (single tokens): 32 rows a workgroup, whose 4 waves take the key
+// Few rows (single tokens): tiles of 32 rows, whose 4 waves take the key
 // tiles in turn, 32 keys each, through LDS of their own (no barrier in the
 // loop), and join their results at the end.  Bound by reading K and V.
 // ---------------------------------------------------------------------------
 
 template <typename E, int DP>
-__global__ __launch_bounds__(256, 1) void k_attention_few(AttnArgs a) {
-  constexpr int kKeys = 32, BM = 32, NW = 4;
+struct Few {
+  static constexpr int kKeys = 32, BM = 32, NW = 4;
   using W = WaveTile<E, DP, kKeys>;
-  constexpr int kBuf = W::kBytes;          // one operand tile
-  constexpr int kLoads = kBuf / 1024;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NW * 4 * kBuf];   // per wave: K0 V0 K1 V1
-  __shared__ float lds_m[NW][32], lds_l[NW][32];
-  static_assert(32 * DP * 4 <= 4 * kBuf, "a wave's O fits in its buffers");
-
-  const Job job = job_of(a, blockIdx.x);
-  const Tile t = find_tile<BM>(a, job.slot);
-  if (!t.any) return;
-  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-
-  const int row = t.row0 + l32;
-  const bool valid = row < t.rows;
-  const int token = row / a.group;
-  const int head = job.head * a.group + (row - token * a.group);
-  const int shift = t.len_k - t.len_q + 1;
-  const int lim = !valid ? 0x7FFFFFFF : a.causal ? token + shift : t.len_k;
-
-  W w;
-  w.init(a, lane);
-  w.load_q(a.q + (t.q0 + token) * a.q_t + head * a.q_h, valid, h, a.D);
-
-  const int last_row = min(t.row0 + BM, t.rows) - 1;
-  const int end = a.causal ? min(t.len_k, last_row / a.group + shift) : t.len_k;
-  const int tiles = (max(end, 0) + kKeys - 1) / kKeys;
-  const int first_lim = a.causal ? min(t.len_k, t.row0 / a.group + shift) : t.len_k;
-  const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * job.split / a.splits);
-  const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (job.split + 1) / a.splits);
-
-  int kv[kLoads], vv[kLoads];
-#pragma unroll
-  for (int n = 0; n < kLoads; ++n) {
-    kv[n] = tile_voff<DP, false>(n, lane, a.k_t, a.D);
-    vv[n] = tile_voff<DP, true>(n, lane, a.v_t, a.D);
-  }
-  const uint32_t base = lds_addr(lds) + wave * 4 * kBuf;
-  const uint16_t* const kp = a.k + t.k0 * a.k_t + job.head * a.k_h;
-  const uint16_t* const vp = a.v + t.k0 * a.v_t + job.head * a.v_h;
-  auto load = [&](int i, int buf) {
-    const int left = t.len_k - i * kKeys;
-    const auto rk = buffer_of(kp + i * kKeys * a.k_t, (left - 1) * a.k_t * 2 + a.D * 2);
-    const auto rv = buffer_of(vp + i * kKeys * a.v_t, (left - 1) * a.v_t * 2 + a.D * 2);
-#pragma unroll
-    for (int n = 0; n < kLoads; ++n) dma_b128(rk, base + 2 * buf * kBuf + n * 1024, kv[n]);
-#pragma unroll
-    for (int n = 0; n < kLoads; ++n) dma_b128(rv, base + (2 * buf + 1) * kBuf + n * 1024, vv[n]);
+  static constexpr int kBuf = W::kBytes;          // one operand tile
+  static constexpr int kLoads = kBuf / 1024;
+  static constexpr int kRow = DP + 4;             // floats of a row of O; the pad spreads rows over banks
+  struct Lds {
+    uint8_t kv[NW * 4 * kBuf];   // per wave: K0 V0 K1 V1, then its O
+    float m[NW][32], l[NW][32];
   };
-  if (t0 + wave < t1) load(t0 + wave, 0);
-  if (t0 + wave + NW < t1) load(t0 + wave + NW, 1);
-  int b = 0;
-  for (int i = t0 + wave; i < t1; i += NW, b ^= 1) {
-    if (i + NW < t1)
-      vm_wait<2 * kLoads>();   // tile i is there, tile i + NW may fly
-    else
-      vm_wait<0>();
-    v16f s[1];
-    w.scores(base + 2 * b * kBuf, s);
-    if ((i + 1) * kKeys > first_lim) w.mask(s, i * kKeys, lim, h);
-    w.raise(w.top(s));
-    v4u p[2];
-    w.weights(s, p);
-    w.accumulate(base + (2 * b + 1) * kBuf, p);
-    // the reads of this buffer are done before it is loaded again
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (i + 2 * NW < t1) load(i + 2 * NW, b);
+
+  // Key tiles [t0, t1) of a tile of rows: leaves O and l of each wave in
+  // LDS, scaled to the rows' common reference.
+  static __device__ __forceinline__ void run(const AttnArgs& a, const Tile& t, int head_k, int t0, int t1, Lds& lds) {
+    const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row = t.row0 + l32;
+    const bool valid = row < t.rows;
+    const int token = row / a.group;
+    const int head = head_k * a.group + (row - token * a.group);
+    const int shift = t.len_k - t.len_q + 1;
+    const int lim = !valid ? 0x7FFFFFFF : a.causal ? token + shift : t.len_k;
+
+    W w;
+    w.init(a, lane);
+    w.load_q(a.q + (t.q0 + token) * a.q_t + head * a.q_h, valid, h, a.D);
+
+    const int last_row = min(t.row0 + BM, t.rows) - 1;
+    const int end = a.causal ? min(t.len_k, last_row / a.group + shift) : t.len_k;
+    t1 = min(t1, (max(end, 0) + kKeys - 1) / kKeys);   // past it no row sees a key
+    const int first_lim = a.causal ? min(t.len_k, t.row0 / a.group + shift) : t.len_k;
+    int kv[kLoads], vv[kLoads];
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      kv[n] = tile_voff<DP, false>(n, lane, a.k_t, a.D);
+      vv[n] = tile_voff<DP, true>(n, lane, a.v_t, a.D);
+    }
+    const uint32_t base = lds_addr(lds.kv) + wave * 4 * kBuf;
+    const uint16_t* const kp = a.k + t.k0 * a.k_t + head_k * a.k_h;
+    const uint16_t* const vp = a.v + t.k0 * a.v_t + head_k * a.v_h;
+    auto load = [&](int i, int buf) {
+      const int left = t.len_k - i * kKeys;
+      const auto rk = buffer_of(kp + i * kKeys * a.k_t, (left - 1) * a.k_t * 2 + a.D * 2);
+      const auto rv = buffer_of(vp + i * kKeys * a.v_t, (left - 1) * a.v_t * 2 + a.D * 2);
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) dma_b128(rk, base + 2 * buf * kBuf + n * 1024, kv[n]);
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) dma_b128(rv, base + (2 * buf + 1) * kBuf + n * 1024, vv[n]);
+    };
+    if (t0 + wave < t1) load(t0 + wave, 0);
+    if (t0 + wave + NW < t1) load(t0 + wave + NW, 1);
+    int b = 0;
+    for (int i = t0 + wave; i < t1; i += NW, b ^= 1) {
+      if (i + NW < t1)
+        vm_wait<2 * kLoads>();   // tile i is there, tile i + NW may fly
+      else
+        vm_wait<0>();
+      v16f s[1];
+      w.scores(base + 2 * b * kBuf, s);
+      if ((i + 1) * kKeys > first_lim) w.mask(s, i * kKeys, lim, h);
+      w.raise(w.top(s));
+      v4u p[2];
+      w.weights(s, p);
+      w.accumulate(base + (2 * b + 1) * kBuf, p);
+      // the reads of this buffer are done before it is loaded again
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (i + 2 * NW < t1) load(i + 2 * NW, b);
+    }
+
+    // join the waves: common reference, then O and l scaled to it
+    const float l = w.row_sum();
+    if (h == 0) lds.m[wave][l32] = w.m;
+    __syncthreads();
+    float m_all = lds.m[0][l32];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) m_all = lds.m[i][l32] > m_all ? lds.m[i][l32] : m_all;
+    const float f = w.m == -INFINITY ? 0.f : exp2_fast((w.m - m_all) * w.sc);
+    float* const mine = reinterpret_cast<float*>(lds.kv + wave * 4 * kBuf);
+    static_assert(32 * kRow * 4 <= 4 * kBuf, "a wave's O fits in its buffers");
+#pragma unroll
+    for (int d = 0; d < W::kDt; ++d)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<v4f*>(mine + l32 * kRow + d * 32 + 8 * j + 4 * h) =
+            v4f{w.acc[d][4 * j] * f, w.acc[d][4 * j + 1] * f, w.acc[d][4 * j + 2] * f, w.acc[d][4 * j + 3] * f};
+    if (h == 0) lds.l[wave][l32] = l * f;
+    __syncthreads();
   }
 
-  // join the waves: common reference, then the sum of the scaled parts
-  float l = w.row_sum();
-  if (h == 0) {
-    lds_m[wave][l32] = w.m;
-    lds_l[wave][l32] = l;
+  // The rows' results, kOf threads a row: ml(row, m, l) by one of them,
+  // o(row, d, four unnormalized values of O, l) by all.
+  template <typename ML, typename O>
+  static __device__ __forceinline__ void finish(const AttnArgs& a, const Tile& t, const Lds& lds, ML ml, O o) {
+    constexpr int kOf = 2 * NW;
+    const int r = threadIdx.x / kOf;
+    if (t.row0 + r >= t.rows) return;
+    float m = lds.m[0][r], l = lds.l[0][r];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) {
+      m = lds.m[i][r] > m ? lds.m[i][r] : m;
+      l += lds.l[i][r];
+    }
+    if (threadIdx.x % kOf == 0) ml(r, m, l);
+    for (int d = threadIdx.x % kOf * 4; d < a.D; d += kOf * 4) {
+      v4f x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < NW; ++i) x += *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(lds.kv + i * 4 * kBuf) + r * kRow + d);
+      o(r, d, x, l);
+    }
+  }
+};
+
+// One workgroup runs through all keys of a tile of rows and a key head.
+template <typename E, int DP>
+__global__ __launch_bounds__(256, 1) void k_attention_few(AttnArgs a) {
+  using F = Few<E, DP>;
+  __shared__ __attribute__((aligned(1024))) typename F::Lds lds;
+  const Job job = job_of(a, blockIdx.x);
+  const Tile t = find_tile<F::BM>(a, job.slot);
+  if (!t.any) return;
+  F::run(a, t, job.head, 0, 0x7FFFFFFF, lds);
+  auto place = [&](int r, int& token, int& head) {
+    token = (t.row0 + r) / a.group;
+    head = job.head * a.group + t.row0 + r - token * a.group;
+    token += t.q0;
+  };
+  F::finish(
+      a, t, lds,
+      [&](int r, float m, float l) {
+        int token, head;
+        place(r, token, head);
+        if (a.lse) a.lse[static_cast<int64_t>(token) * a.heads_q + head] = lse_of(m, l, a.scale);
+      },
+      [&](int r, int d, v4f x, float l) {
+        int token, head;
+        place(r, token, head);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        *reinterpret_cast<v2u*>(a.o + token * a.o_t + head * a.o_h + d) =
+            v2u{E::pack2(x[0] * inv, x[1] * inv), E::pack2(x[2] * inv, x[3] * inv)};
+      });
+}
+
+// Few rows and few heads: the pieces of work (a tile of 32 rows, a tile of
+// 32 keys, a key head), laid in a line by head, sequence, rows and keys, are
+// cut into a.spread equal parts, one a workgroup, whatever the sequences'
+// lengths.  A part may run over several tiles of rows; its share of each, its
+// "result" p = workgroup + (tiles of rows before this one), is written for
+// k_attention_spread_join (p grows with every step along the line, so no two
+// results share one).
+constexpr int kSpreadBatch = 512;
+
+template <typename E, int DP>
+__global__ __launch_bounds__(256, 1) void k_attention_spread(AttnArgs a) {
+  using F = Few<E, DP>;
+  __shared__ __attribute__((aligned(1024))) typename F::Lds lds;
+  __shared__ int64_t before[kSpreadBatch + 1];
+  __shared__ int32_t before_q[kSpreadBatch + 1];
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    int64_t sum = 0;
+    int sum_q = 0;
+    for (int i0 = 0; i0 < a.batch; i0 += 64) {
+      int64_t n = 0;
+      int nq = 0;
+      if (i0 + lane < a.batch) {
+        const Tile t = sequence(a, i0 + lane);
+        nq = (t.rows + 31) >> 5;
+        n = static_cast<int64_t>(nq) * ((t.len_k + 31) >> 5);
+      }
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int64_t x = __shfl_up(n, o);
+        const int xq = __shfl_up(nq, o);
+        if (lane >= o) {
+          n += x;
+          nq += xq;
+        }
+      }
+      if (i0 + lane < a.batch) {
+        before[i0 + lane + 1] = sum + n;
+        before_q[i0 + lane + 1] = sum_q + nq;
+      }
+      sum += __shfl(n, 63);
+      sum_q += __shfl(nq, 63);
+    }
+    if (lane == 0) {
+      before[0] = 0;
+      before_q[0] = 0;
+    }
   }
   __syncthreads();
-  float m_all = lds_m[0][l32];
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= a.batch; i += 256) {
+      a.before[i] = before[i];
+      a.before_q[i] = before_q[i];
+    }
+  const int64_t per_head = before[a.batch], total = per_head * a.heads_k;
+  const int tiles_q = before_q[a.batch];
+  int64_t at = total * blockIdx.x / a.spread;
+  const int64_t end = total * (blockIdx.x + 1) / a.spread;
+  while (at < end) {
+    const int head = static_cast<int>(at / per_head);
+    const int64_t r = at - head * per_head;
+    const int seq = last_before(a.batch, [&](int i) { return before[i] <= r; });
+    Tile t = sequence(a, seq);
+    const int tiles_k = (t.len_k + 31) >> 5;
+    const int rest = static_cast<int>(r - before[seq]);
+    const int qt = rest / tiles_k, k0 = rest - qt * tiles_k;
+    const int k1 = static_cast<int>(end - at < tiles_k - k0 ? k0 + (end - at) : tiles_k);
+    t.row0 = qt * 32;
+    const int64_t p = static_cast<int64_t>(blockIdx.x) + static_cast<int64_t>(head) * tiles_q + before_q[seq] + qt;
+    if (p >= a.results) return;   // only with starts that do not rise
+    F::run(a, t, head, k0, k1, lds);
+    F::finish(
+        a, t, lds, [&](int row, float m, float l) { a.part_ml[p * 32 + row] = make_float2(m, l); },
+        [&](int row, int d, v4f x, float) { *reinterpret_cast<v4f*>(a.part_o + (p * 32 + row) * a.D + d) = x; });
+    at += k1 - k0;
+    __syncthreads();   // LDS is read out before the next loads
+  }
+}
+
+// Join of the results of one row, a workgroup's 4 waves taking them in turn,
+// always in the same order.
+template <typename E>
+__global__ __launch_bounds__(256) void k_attention_spread_join(AttnArgs a) {
+  __shared__ float top[4], sums[4], scale[256];
+  __shared__ int64_t where[256];
+  __shared__ v2f part[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int token = blockIdx.x / a.heads_q, hq = blockIdx.x - token * a.heads_q;
+  int seq = 0;
+  if (a.batch > 1) seq = last_before(a.batch, [&](int i) { return a.cu_q[i] <= token; });
+  const Tile t = sequence(a, seq);
+  const int64_t per_head = a.before[a.batch], total = per_head * a.heads_k;
+  const int head = hq / a.group, tiles_k = (t.len_k + 31) >> 5;
+  const int row = (token - t.q0) * a.group + hq - head * a.group;
+  const int qt = row >> 5;
+  int n = 0;   // workgroups from the first to the last that took part
+  int64_t first = 0, b0 = 0, b1 = 0, tile = 0;
+  if (tiles_k > 0 && row >= 0 && row < t.rows) {
+    b0 = head * per_head + a.before[seq] + static_cast<int64_t>(qt) * tiles_k;
+    b1 = b0 + tiles_k;
+    // workgroup w begins at floor(total w / spread)
+    first = ((b0 + 1) * a.spread - 1) / total;
+    n = static_cast<int>((b1 * a.spread - 1) / total - first) + 1;
+    tile = static_cast<int64_t>(head) * a.before_q[a.batch] + a.before_q[seq] + qt;
+  }
+  // one result a thread (no more workgroups than threads)
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (static_cast<int>(threadIdx.x) < n) {
+    const int64_t w = first + threadIdx.x;
+    const int64_t from = total * w / a.spread, to = total * (w + 1) / a.spread;
+    const int64_t at = (w + tile) * 32 + (row & 31);
+    where[threadIdx.x] = at;
+    // (a workgroup without a share wrote nothing)
+    if ((from > b0 ? from : b0) < (to < b1 ? to : b1) && at < a.results * 32) ml = a.part_ml[at];
+  }
+  float m = ml.x;
 #pragma unroll
-  for (int i = 1; i < NW; ++i) m_all = lds_m[i][l32] > m_all ? lds_m[i][l32] : m_all;
-  const float f = w.m == -INFINITY ? 0.f : exp2_fast((w.m - m_all) * w.sc);
-  constexpr int kRow = DP + 4;   // floats; the pad spreads rows over banks
-  float* const mine = reinterpret_cast<float*>(lds + wave * 4 * kBuf);
-  static_assert(32 * kRow * 4 <= 4 * kBuf, "a wave's O fits in its buffers");
-#pragma unroll
-  for (int d = 0; d < W::kDt; ++d)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<v4f*>(mine + l32 * kRow + d * 32 + 8 * j + 4 * h) =
-          v4f{w.acc[d][4 * j] * f, w.acc[d][4 * j + 1] * f, w.acc[d][4 * j + 2] * f, w.acc[d][4 * j + 3] * f};
-  if (h == 0) lds_l[wave][l32] = l * f;
+  for (int o = 32; o; o >>= 1) {
+    const float x = __shfl_xor(m, o);
+    m = x > m ? x : m;
+  }
+  if (lane == 0) top[wave] = m;
   __syncthreads();
-  // kOf threads a row, each every kOf-th 4 columns
-  constexpr int kOf = 2 * NW;
-  const int r = threadIdx.x / kOf;
-  const int rr = t.row0 + r;
-  if (rr >= t.rows) return;
-  float m_row = lds_m[0][r], l_row = lds_l[0][r];
 #pragma unroll
-  for (int i = 1; i < NW; ++i) {
-    m_row = lds_m[i][r] > m_row ? lds_m[i][r] : m_row;
-    l_row += lds_l[i][r];
-  }
-  const int tok = rr / a.group;
-  const int hd = job.head * a.group + rr - tok * a.group;
-  const int64_t out_row = static_cast<int64_t>(t.q0 + tok) * a.heads_q + hd;
-  const int64_t part = static_cast<int64_t>(job.split) * a.total_q * a.heads_q + out_row;
-  const bool whole = a.splits == 1;
-  if (threadIdx.x % kOf == 0) {
-    if (!whole)
-      a.part_ml[part] = make_float2(m_row, l_row);
-    else if (a.lse)
-      a.lse[out_row] = lse_of(m_row, l_row, a.scale);
-  }
-  const float inv = l_row == 0.f ? 0.f : 1.f / l_row;
-  for (int d = threadIdx.x % kOf * 4; d < a.D; d += kOf * 4) {
-    v4f x = {0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < 4; ++i) m = top[i] > m ? top[i] : m;
+  const float f = ml.y == 0.f ? 0.f : exp2_fast((ml.x - m) * (a.scale * kLog2e));
+  float l = ml.y * f;
+  scale[threadIdx.x] = f;
 #pragma unroll
-    for (int i = 0; i < NW; ++i) x += *reinterpret_cast<const v4f*>(reinterpret_cast<float*>(lds + i * 4 * kBuf) + r * kRow + d);
-    if (whole)
-      *reinterpret_cast<v2u*>(a.o + (t.q0 + tok) * a.o_t + hd * a.o_h + d) =
-          v2u{E::pack2(x[0] * inv, x[1] * inv), E::pack2(x[2] * inv, x[3] * inv)};
-    else
-      *reinterpret_cast<v4f*>(a.part_o + part * a.D + d) = x;
+  for (int o = 32; o; o >>= 1) l += __shfl_xor(l, o);
+  if (lane == 0) sums[wave] = l;
+  __syncthreads();
+  l = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+  v2f x = {0.f, 0.f};
+  const int d = 2 * lane;
+  if (d < a.D) {
+#pragma unroll 4
+    for (int i = wave; i < n; i += 4)
+      if (scale[i] != 0.f) x += *reinterpret_cast<const v2f*>(a.part_o + where[i] * a.D + d) * scale[i];
   }
+  part[wave][lane] = x;
+  __syncthreads();
+  if (wave) return;
+  x = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (d < a.D)
+    *reinterpret_cast<uint32_t*>(a.o + token * a.o_t + hq * a.o_h + d) = E::pack2(x[0] * inv, x[1] * inv);
+  if (a.lse && lane == 0) a.lse[blockIdx.x] = lse_of(m, l, a.scale);
 }
 
 // Join of the splits: a wave per row, in the order of the splits.  A split
@@ -702,10 +878,14 @@ __global__ __launch_bounds__(256) void k_attention_join(AttnArgs a) {
 }
 
 struct Plan {
-  int waves;     // rows a workgroup takes / 32; 0: k_attention_few
-  int splits;
+  int waves;     // rows a workgroup takes / 32; 0: k_attention_few or k_attention_spread
+  int splits;    // of a tile's keys, waves > 0
+  int spread;    // workgroups of k_attention_spread, or 0
   size_t bytes;
 };
+
+// bytes of k_attention_spread's counts, before its results
+size_t spread_head(int batch) { return (static_cast<size_t>(batch + 1) * 12 + 15) & ~size_t(15); }
 
 // The schedule from the sizes the host knows.  Lengths are on the device, so
 // the mean stands for them; every schedule is right for any lengths.
@@ -723,12 +903,25 @@ Plan plan_for(int total_q, int total_k, int batch, int heads_q, int heads_k, int
   // read the keys half as often (4608 x 24 heads 270 -> 255 us).
   const bool few = mean_rows <= 64 || (mean_rows <= 256 && units(32) <= 256);
   p.waves = few ? 0 : causal || units(256) < 256 || mean_keys < 1024 ? 4 : 8;
+  p.splits = 1;
+  p.spread = 0;
+  p.bytes = 0;
   const int64_t n = units(p.waves ? p.waves * 32 : 32);
-  const int64_t want = p.waves ? 256 : 1024, keys = p.waves ? 512 : 256;
-  int64_t s = n >= want / 2 ? 1 : (want + n - 1) / n;
-  if (s > mean_keys / keys) s = mean_keys / keys;
+  if (p.waves == 0) {
+    // Where the tiles of rows would not give every CU two workgroups, one
+    // workgroup a CU with equal shares of at least 8 tiles of keys, two a wave.
+    int64_t w = n / heads_k * ((mean_keys + 31) / 32) * heads_k / 8;
+    if (w > 256) w = 256;
+    if (n >= 512 || batch > kSpreadBatch || w <= n) return p;
+    p.spread = static_cast<int>(w);
+    const int64_t results = w + (rows / 32 + batch) * heads_k;
+    p.bytes = spread_head(batch) + static_cast<size_t>(results) * 32 * (D + 2) * 4;
+    return p;
+  }
+  int64_t s = n >= 128 ? 1 : (256 + n - 1) / n;
+  if (s > mean_keys / 512) s = mean_keys / 512;
   p.splits = static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
-  p.bytes = p.splits == 1 ? 0 : static_cast<size_t>(p.splits) * total_q * heads_q * (D + 2) * 4;
+  if (p.splits > 1) p.bytes = static_cast<size_t>(p.splits) * total_q * heads_q * (D + 2) * 4;
   return p;
 }
 
@@ -736,6 +929,7 @@ template <typename E>
 int launch(AttnArgs a, const Plan& p, hipStream_t stream) {
   const int bm = p.waves ? p.waves * 32 : 32;
   a.splits = p.splits;
+  a.spread = p.spread;
   a.slots = static_cast<int>(static_cast<int64_t>(a.total_q) * a.group / bm) + a.batch;
   const dim3 grid(static_cast<unsigned>(a.slots) * a.heads_k * a.splits);
   const bool wide = a.D > 64;
@@ -749,6 +943,12 @@ int launch(AttnArgs a, const Plan& p, hipStream_t stream) {
       k_attention<E, 128, 4><<<grid, 256, 0, stream>>>(a);
     else
       k_attention<E, 64, 4><<<grid, 256, 0, stream>>>(a);
+  } else if (p.spread) {
+    if (wide)
+      k_attention_spread<E, 128><<<p.spread, 256, 0, stream>>>(a);
+    else
+      k_attention_spread<E, 64><<<p.spread, 256, 0, stream>>>(a);
+    k_attention_spread_join<E><<<dim3(static_cast<unsigned>(a.total_q) * a.heads_q), 256, 0, stream>>>(a);
   } else {
     if (wide)
       k_attention_few<E, 128><<<grid, 256, 0, stream>>>(a);
@@ -777,13 +977,20 @@ int svdq_launch_attention(const void* q, const void* k, const void* v, void* o, 
                           int head_dim, const int64_t* strides, float scale, int causal, int dtype, void* workspace,
                           size_t workspace_bytes, void* stream) {
   Plan p = plan_for(total_q, total_k, batch, heads_q, heads_k, head_dim, causal);
-  if (!workspace || workspace_bytes < p.bytes) p.splits = 1;
+  if (!workspace || workspace_bytes < p.bytes) p.splits = 1, p.spread = 0;
   AttnArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);
   a.v = static_cast<const uint16_t*>(v);
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
+  if (p.spread) {
+    a.before = static_cast<int64_t*>(workspace);
+    a.before_q = reinterpret_cast<int32_t*>(a.before + batch + 1);
+    a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + spread_head(batch));
+    a.results = p.spread + (static_cast<int64_t>(total_q) * (heads_q / heads_k) / 32 + batch) * heads_k;
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + a.results * 32 * head_dim);
+  }
   if (p.splits > 1) {
     a.part_o = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(p.splits) * total_q * heads_q * head_dim);
