@@ -13,7 +13,13 @@ import torch
 from ._lib import BF16, F16, check, lib
 
 _DTYPE = {torch.bfloat16: BF16, torch.float16: F16}
-_Strides = ctypes.c_int64 * 8
+
+
+@functools.lru_cache(maxsize=4096)
+def _strides(*values):
+    """The C array of these strides."""
+    return (ctypes.c_int64 * len(values))(*values)
+
 
 # The smallest calls take about as long on the host as on the device, so the
 # arguments of a valid call are looked at once, cheaply; _refuse finds the
@@ -24,16 +30,16 @@ def _operand(t, dims, name, layout):
     """(dtype code, device index) of a call's first operand."""
     try:
         code, device = _DTYPE.get(t.dtype), t.get_device()
-        fine = t.dim() == dims and device >= 0 and (t.stride(-1) == 1 or t.shape[-1] <= 1)
+        stride = t.stride()
+        if code is not None and device >= 0 and len(stride) == dims and (stride[-1] == 1 or t.shape[-1] <= 1):
+            return code, device
     except (AttributeError, RuntimeError):
         raise TypeError(f"{name}: expected a device tensor {layout}") from None
     if code is None:
         raise TypeError(f"{name}: expected a bfloat16 or float16 tensor, got {t.dtype}")
-    if not fine:
-        if t.dim() == dims and device >= 0:
-            raise ValueError(f"{name}: the last dimension must be contiguous")
-        raise TypeError(f"{name}: expected a device tensor {layout}")
-    return code, device
+    if len(stride) == dims and device >= 0:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    raise TypeError(f"{name}: expected a device tensor {layout}")
 
 
 def _like(t, dtype, device, shape, name):
@@ -58,11 +64,11 @@ def _ptr(t):
 
 def _call(device, fn, *args):
     """Run a library call with `device` current, on its current stream."""
-    if device != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    else:
+    if device == _current_device():
         status = fn(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(device))
     if status:
         check(status)
 
@@ -70,6 +76,7 @@ def _call(device, fn, *args):
 # the current stream's handle without a Stream object around it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _workspace(workspace, nbytes, device):
@@ -116,9 +123,12 @@ def attention(q, k, v, *, cu_seqlens_q=None, cu_seqlens_k=None, causal: bool = F
     gives o = 0, lse = -inf."""
     code, device = _operand(q, 3, "q", "[tokens][heads][head_dim]")
     total_q, heads_q, head_dim = q.shape
-    _operand(k, 3, "k", "[tokens][heads][head_dim]")
-    total_k, heads_k, _ = shape = k.shape
     dtype = q.dtype
+    try:
+        shape = k.shape
+        total_k, heads_k, _ = shape
+    except (AttributeError, ValueError):
+        raise TypeError("k: expected a device tensor [tokens][heads][head_dim]") from None
     _like(k, dtype, device, (total_k, heads_k, head_dim), "k")
     _like(v, dtype, device, shape, "v")
     batch = 1
@@ -132,25 +142,29 @@ def attention(q, k, v, *, cu_seqlens_q=None, cu_seqlens_k=None, causal: bool = F
             if total_k != total_q:
                 raise ValueError("cu_seqlens_k is needed where q and k have different numbers of tokens")
             cu_seqlens_k = cu_seqlens_q
-        elif _cu_seqlens(cu_seqlens_k, device, "cu_seqlens_k") != batch:
+        elif cu_seqlens_k is not cu_seqlens_q and _cu_seqlens(cu_seqlens_k, device, "cu_seqlens_k") != batch:
             raise ValueError("cu_seqlens_q and cu_seqlens_k must have the same number of entries")
         cu_q, cu_k = cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr()
+    sq, sk, sv, so = q.stride(), k.stride(), v.stride(), (heads_q * head_dim, head_dim)
     if out is None:
         out = q.new_empty((total_q, heads_q, head_dim))
     else:
         _like(out, dtype, device, q.shape, "out")
+        so = out.stride()
     lse = q.new_empty((total_q, heads_q), dtype=torch.float32) if return_lse else None
-    # token and head strides; dimensions of size 1 have none, and get those of a dense tensor
-    dense_q, dense_k = heads_q * head_dim, heads_k * head_dim
-    st = []
-    for t, n, h, dense in ((q, total_q, heads_q, dense_q), (k, total_k, heads_k, dense_k), (v, total_k, heads_k, dense_k),
-                           (out, total_q, heads_q, dense_q)):
-        a, b, _ = t.stride()
-        st += (a if n > 1 else dense, b if h > 1 else head_dim)
+    if total_q > 1 and total_k > 1 and heads_q > 1 and heads_k > 1:
+        strides = _strides(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1])
+    else:
+        # dimensions of size 1 have no stride, and get that of a dense tensor
+        st = []
+        for (token, head, *_), n, h in ((sq, total_q, heads_q), (sk, total_k, heads_k), (sv, total_k, heads_k),
+                                        (so, total_q, heads_q)):
+            st += (token if n > 1 else h * head_dim, head if h > 1 else head_dim)
+        strides = _strides(*st)
     nbytes = 0 if workspace is None else attention_workspace_size(total_q, total_k, batch, heads_q, heads_k, head_dim)
     ws, ws_bytes, _keep = _workspace(workspace, nbytes, device)
     _call(device, lib.svdq_attention, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), cu_q, cu_k,
-          batch, total_q, total_k, heads_q, heads_k, head_dim, _Strides(*st),
+          batch, total_q, total_k, heads_q, heads_k, head_dim, strides,
           head_dim ** -0.5 if scale is None else float(scale), 1 if causal else 0, code, ws, ws_bytes)
     return (out, lse) if return_lse else out
 
@@ -214,10 +228,12 @@ def linear16(x, w, bias=None, *, activation: str = "none", gate=None, residual=N
     defaults to M / groups).  activation: "none", "gelu" (tanh form) or
     "silu".  Rows may be strided.  `out` may be `residual`."""
     code, device = _operand(x, 2, "x", "[M][K]")
-    _operand(w, 2, "w", "[N][K]")
     M, K = x.shape
-    N = w.shape[0]
     dtype = x.dtype
+    try:
+        N, _ = w.shape
+    except (AttributeError, ValueError):
+        raise TypeError("w: expected a device tensor [N][K]") from None
     _like(w, dtype, device, (N, K), "w")
     act = ACTIVATIONS.get(activation)
     if act is None:
