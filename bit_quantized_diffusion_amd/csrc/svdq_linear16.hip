@@ -447,14 +447,19 @@ __global__ __launch_bounds__(256) void k_linear16_join(LinArgs a) {
 
 // ---------------------------------------------------------------------------
 // Few rows (M <= 32): bound by reading W once.  A workgroup takes 32
-// channels; its 4 waves take the stages of 128 k in turn, each through LDS of
-// its own (kDepth stages in flight, no barrier in the loop), and join at the
-// end.  XL: 1 KB loads that bring in the rows of x (4 rows each).
+// channels; its waves take the stages of 128 k in turn, each through LDS of
+// its own (two stages in flight, no barrier in the loop), and join at the
+// end.  XL: 1 KB loads that bring in the rows of x (4 rows each).  Two
+// workgroups share a CU's LDS, so that one reads while the other starts or
+// joins (2 x 18432 x 3072: 26.7 us with three stages and one workgroup a CU,
+// 23.1 with two and two: 4.9 TB/s); from 9 rows on that takes two waves, which
+// pays where there are more workgroups than CUs (16 x 9216 x 3072 18.5 -> 15.9
+// us, 4 x 3072 x 15360 27 -> 36).
 // ---------------------------------------------------------------------------
 
-template <typename E, int XL>
-__global__ __launch_bounds__(256, 1) void k_linear16_few(LinArgs a) {
-  constexpr int kWaves = 4, kDepth = XL > 4 ? 2 : 3;
+template <typename E, int XL, int NW>
+__global__ __launch_bounds__(NW * 64, 1) void k_linear16_few(LinArgs a) {
+  constexpr int kWaves = NW, kDepth = 2;
   constexpr int kRowB = 256, kStage = (32 + 4 * XL) * kRowB;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * kDepth * kStage];
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
@@ -510,9 +515,7 @@ __global__ __launch_bounds__(256, 1) void k_linear16_few(LinArgs a) {
   int slot = 0;
   for (int st = wave; st < stages; st += kWaves) {
     const int more = (stages - 1 - st) / kWaves;   // stages of this wave still in flight
-    if (kDepth == 3 && more >= 2)
-      vm_wait<2 * (8 + XL)>();
-    else if (more >= 1)
+    if (more >= 1)
       vm_wait<8 + XL>();
     else
       vm_wait<0>();
@@ -535,16 +538,17 @@ __global__ __launch_bounds__(256, 1) void k_linear16_few(LinArgs a) {
         v4f{acc[0][4 * q] + acc[1][4 * q], acc[0][4 * q + 1] + acc[1][4 * q + 1], acc[0][4 * q + 2] + acc[1][4 * q + 2],
             acc[0][4 * q + 3] + acc[1][4 * q + 3]};
   __syncthreads();
-  const int m = threadIdx.x >> 2;
-  if (m >= a.M || m >= 32) return;
-  Columns<E> col;
-  col.init(a, n0 + (threadIdx.x & 3) * 8);
-  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  // a thread takes 8 channels of every 16 kWaves-th row
+  for (int m = threadIdx.x >> 2; m < a.M; m += 16 * kWaves) {
+    Columns<E> col;
+    col.init(a, n0 + (threadIdx.x & 3) * 8);
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i)
+    for (int i = 0; i < kWaves; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] += reinterpret_cast<float*>(lds)[(i * 32 + m) * kRow + (threadIdx.x & 3) * 8 + e];
-  col.finish(a, m, f);
+      for (int e = 0; e < 8; ++e) f[e] += reinterpret_cast<float*>(lds)[(i * 32 + m) * kRow + (threadIdx.x & 3) * 8 + e];
+    col.finish(a, m, f);
+  }
 }
 
 // Schedules.  `slots`: workgroups the device holds at once; `light` and
@@ -616,14 +620,19 @@ int launch(LinArgs a, bool aligned, size_t workspace, hipStream_t stream) {
   a.splits = 1;
   if (aligned && a.M <= kFewRows) {
     const unsigned blocks = (a.N + 31) / 32;
+    const bool many = blocks > 256;
     if (a.M <= 4)
-      k_linear16_few<E, 1><<<blocks, 256, 0, stream>>>(a);
+      k_linear16_few<E, 1, 4><<<blocks, 256, 0, stream>>>(a);
     else if (a.M <= 8)
-      k_linear16_few<E, 2><<<blocks, 256, 0, stream>>>(a);
+      k_linear16_few<E, 2, 4><<<blocks, 256, 0, stream>>>(a);
+    else if (a.M <= 16 && many)
+      k_linear16_few<E, 4, 2><<<blocks, 128, 0, stream>>>(a);
     else if (a.M <= 16)
-      k_linear16_few<E, 4><<<blocks, 256, 0, stream>>>(a);
+      k_linear16_few<E, 4, 4><<<blocks, 256, 0, stream>>>(a);
+    else if (many)
+      k_linear16_few<E, 8, 2><<<blocks, 128, 0, stream>>>(a);
     else
-      k_linear16_few<E, 8><<<blocks, 256, 0, stream>>>(a);
+      k_linear16_few<E, 8, 4><<<blocks, 256, 0, stream>>>(a);
     return static_cast<int>(hipGetLastError());
   }
   const Plan p = plan_for(a.M, a.N, a.K, aligned, workspace);

@@ -51,6 +51,12 @@ def test_few_rows(m, n, k):
     check(m, n, k, BF if m % 2 else HF, act="silu" if m % 3 else "none")
 
 
+@pytest.mark.parametrize("m", [1, 7, 9, 13, 16, 17, 30, 32])
+def test_few_rows_many_channels(m):
+    """More workgroups than CUs: two waves each from 9 rows on."""
+    check(m, 8500, 200, act="gelu", gate=1, residual=True)
+
+
 @pytest.mark.parametrize("m,n,k", [(33, 128, 64), (64, 64, 72), (127, 129, 200), (128, 128, 8), (129, 257, 1024), (333, 520, 136),
                                    (300, 40, 16), (40, 1, 64), (513, 130, 2048)])
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "f16"])
