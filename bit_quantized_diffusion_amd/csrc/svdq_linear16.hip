@@ -346,15 +346,16 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void k_linear16(LinArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// The same for rows at any 2-byte alignment and any K: tiles of 128 x 128,
-// stages of 64 fetched with unaligned loads into registers one stage ahead.
-// A row of a stage is 128 bytes, two rows share the LDS banks; chunk c of row
-// r sits at chunk c ^ ((r / 2) % 8).
+// The same for rows at any 2-byte alignment and any K: tiles of B x B, 2 x 2
+// waves, stages of 64 fetched with unaligned loads into registers, AHEAD
+// stages before they go to LDS, and from there double-buffered.  Rows past
+// the tile repeat the last one (their results are not stored); past K both
+// operands are zero.  LDS rows as above.
 // ---------------------------------------------------------------------------
 
-template <typename E>
+template <typename E, int B, int AHEAD>
 __global__ __launch_bounds__(256, 2) void k_linear16_any(LinArgs a) {
-  constexpr int B = 128, kRowB = 128, kStage = 2 * B * kRowB, kLoads = kStage / 1024 / 4;
+  constexpr int kRowB = 128, kStage = 2 * B * kRowB, kLoads = kStage / 1024 / 4, kT = B / 32;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
   const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -369,52 +370,67 @@ __global__ __launch_bounds__(256, 2) void k_linear16_any(LinArgs a) {
   const uint16_t* const p = is_x ? a.x + m0 * a.ldx : a.w + n0 * a.ldw;
   const int64_t ld = is_x ? a.ldx : a.ldw;
   const int rows = is_x ? a.M - m0 : a.N - n0;
-  v4u held[kLoads];
-  auto fetch = [&](int st) {
+  int64_t at[kLoads];
 #pragma unroll
-    for (int n = 0; n < kLoads; ++n) {
-      const int r = ((wave & 1) * kLoads + n) * 8 + (lane >> 3);
-      const int k = st * 64 + ((lane & 7) ^ ((r >> 1) & 7)) * 8;
-      held[n] = v4u{0, 0, 0, 0};
-      if (r < rows && k < a.K) held[n] = load8(p + r * ld + k, a.K - k);
+  for (int n = 0; n < kLoads; ++n) {
+    const int r = ((wave & 1) * kLoads + n) * 8 + (lane >> 3);
+    at[n] = min(r, rows - 1) * ld + ((lane & 7) ^ ((r >> 1) & 7)) * 8;
+  }
+  v4u held[AHEAD][kLoads];
+  auto fetch = [&](int st, v4u (&v)[kLoads]) {
+    if (st * 64 + 64 <= a.K) {
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) v[n] = load8(p + at[n] + st * 64);
+    } else {
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) {
+        const int r = ((wave & 1) * kLoads + n) * 8 + (lane >> 3);
+        const int left = a.K - st * 64 - ((lane & 7) ^ ((r >> 1) & 7)) * 8;
+        v[n] = v4u{0, 0, 0, 0};
+        if (left > 0) v[n] = load8(p + at[n] + st * 64, left);
+      }
     }
   };
-  auto put = [&](int buf) {
+  v4f acc[kT][kT];
 #pragma unroll
-    for (int n = 0; n < kLoads; ++n)
-      *reinterpret_cast<v4u*>(lds + buf * kStage + (wave * kLoads + n) * 1024 + lane * 16) = held[n];
-  };
-  v4f acc[4][4];
+  for (int i = 0; i < kT; ++i)
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < kT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  auto stage = [&](int st, v4u (&v)[kLoads]) {
+    uint8_t* const buf = lds + (st & 1) * kStage;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  fetch(s0);
-  put(0);
-  __syncthreads();
-  for (int st = s0; st < s1; ++st) {
-    const int b = (st - s0) & 1;
-    if (st + 1 < s1) fetch(st + 1);
-    const uint8_t* const pw = lds + b * kStage + (wn * 64 + l16) * kRowB;
-    const uint8_t* const px = lds + b * kStage + (B + wm * 64 + l16) * kRowB;
+    for (int n = 0; n < kLoads; ++n) *reinterpret_cast<v4u*>(buf + (wave * kLoads + n) * 1024 + lane * 16) = v[n];
+    // the other buffer was read out before this wave's writes of the stage
+    // before; loads in flight stay in flight
+    lds_barrier();
+    if (st + AHEAD < s1) fetch(st + AHEAD, v);
+    const uint8_t* const pw = buf + (wn * kT * 16 + l16) * kRowB;
+    const uint8_t* const px = buf + (B + wm * kT * 16 + l16) * kRowB;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int c = ((4 * s + q) ^ (l16 >> 1)) << 4;
-      v4u fw[4], fx[4];
+      v4u fw[kT], fx[kT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kT; ++i) {
         fw[i] = *reinterpret_cast<const v4u*>(pw + i * 16 * kRowB + c);
         fx[i] = *reinterpret_cast<const v4u*>(px + i * 16 * kRowB + c);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = E::mfma16(fw[i], fx[j], acc[i][j]);
+        for (int j = 0; j < kT; ++j) acc[i][j] = E::mfma16(fw[i], fx[j], acc[i][j]);
     }
-    if (st + 1 < s1) put(b ^ 1);
-    __syncthreads();
+  };
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (s0 + i < s1) fetch(s0 + i, held[i]);
+  for (int st = s0; st < s1; st += AHEAD) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (st + i < s1) stage(st + i, held[i]);
   }
-  epilogue<E, B, B, 2, 2, 4, 4, staged_tiles(4, 2 * 16 * B * 4, 2 * kStage)>(a, acc, lds, m0, n0);
+  lds_barrier();
+  epilogue<E, B, B, 2, 2, kT, kT, staged_tiles(kT, 2 * 16 * B * 4, 2 * kStage)>(a, acc, lds, m0, n0);
 }
 
 // Sum of the splits in their order, then the epilogue: 8 channels a thread.
@@ -559,13 +575,14 @@ struct Shape {
   int bn, bm, slots;
   float light, full, fixed;
 };
-enum { k256, k128, k128Deep, k64, kAny, kShapes };
+enum { k256, k128, k128Deep, k64, kAny128, kAny64, kShapes };
 constexpr Shape kShape[kShapes] = {
     {256, 256, 256, 1.10f, 1.45f, 8.f},   // 8 waves
     {128, 128, 512, 0.50f, 0.83f, 5.f},   // 4 waves, two workgroups a CU
     {128, 128, 256, 0.36f, 0.42f, 5.f},   // 8 waves, loads two stages further ahead
     {64, 64, 512, 0.20f, 0.33f, 4.f},     // 4 waves, one stage further ahead
-    {128, 128, 512, 0.60f, 1.20f, 5.f},   // k_linear16_any
+    {128, 128, 512, 1.00f, 1.60f, 5.f},   // k_linear16_any, two stages ahead
+    {64, 64, 512, 0.38f, 0.65f, 4.f},     // k_linear16_any, three stages ahead
 };
 constexpr int kMaxSplits = 8;
 
@@ -580,9 +597,9 @@ struct Plan {
 // reads and writes them once more.
 Plan plan_for(int M, int N, int K, bool aligned, size_t most) {
   const int stages = (K + 63) / 64;
-  Plan best{kAny, 1, stages, 0};
+  Plan best{kAny64, 1, stages, 0};
   float least = INFINITY;
-  for (int i = aligned ? 0 : kAny; i < (aligned ? kAny : kShapes); ++i) {
+  for (int i = aligned ? 0 : kAny128; i < (aligned ? kAny128 : kShapes); ++i) {
     const Shape& c = kShape[i];
     const float tiles = static_cast<float>((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
     for (int s = 1; s <= kMaxSplits && s <= stages; ++s) {
@@ -643,7 +660,8 @@ int launch(LinArgs a, bool aligned, size_t workspace, hipStream_t stream) {
     case k128: start<E, 128, 128, 2, 2, 0>(a, stream); break;
     case k128Deep: start<E, 128, 128, 2, 4, 2>(a, stream); break;
     case k64: start<E, 64, 64, 2, 2, 1>(a, stream); break;
-    default: k_linear16_any<E><<<tiles(a, 128, 128), 256, 0, stream>>>(a);
+    case kAny128: k_linear16_any<E, 128, 2><<<tiles(a, 128, 128), 256, 0, stream>>>(a); break;
+    default: k_linear16_any<E, 64, 3><<<tiles(a, 64, 64), 256, 0, stream>>>(a);
   }
   if (a.splits > 1) {
     const int64_t n = static_cast<int64_t>((a.N + 7) / 8) * a.M;
