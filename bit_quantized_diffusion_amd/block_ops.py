@@ -13,6 +13,7 @@ import torch
 from ._lib import BF16, F16, check, lib
 
 _DTYPE = {torch.bfloat16: BF16, torch.float16: F16}
+_MOST = 2 ** 31 - 2 ** 16
 
 
 @functools.lru_cache(maxsize=4096)
@@ -21,9 +22,8 @@ def _strides(*values):
     return (ctypes.c_int64 * len(values))(*values)
 
 
-# The smallest calls take about as long on the host as on the device, so the
-# arguments of a valid call are looked at once, cheaply; _refuse finds the
-# words for one that is not.
+# The smallest calls take longer on the host than on the device, so a valid
+# argument is passed by one cheap look; the words are found for one that is not.
 
 
 def _operand(t, dims, name, layout):
@@ -118,7 +118,8 @@ def attention(q, k, v, *, cu_seqlens_q=None, cu_seqlens_k=None, causal: bool = F
     from the sequences' ends (query i sees keys j <= i + len_k - len_q).
     scale defaults to head_dim ** -0.5.
 
-    Returns o (like q, contiguous unless `out` is given) or, with
+    Returns o (like q, contiguous unless `out` is given, which overlaps none
+    of q, k and v) or, with
     return_lse, (o, lse fp32 [total_q][heads_q]).  A query that sees no key
     gives o = 0, lse = -inf."""
     code, device = _operand(q, 3, "q", "[tokens][heads][head_dim]")
@@ -131,6 +132,8 @@ def attention(q, k, v, *, cu_seqlens_q=None, cu_seqlens_k=None, causal: bool = F
         raise TypeError("k: expected a device tensor [tokens][heads][head_dim]") from None
     _like(k, dtype, device, (total_k, heads_k, head_dim), "k")
     _like(v, dtype, device, shape, "v")
+    if total_q > _MOST or total_k > _MOST:
+        raise ValueError("attention: more tokens than the library counts (2^31 - 2^16)")
     batch = 1
     cu_q = cu_k = None
     if cu_seqlens_q is None:
@@ -165,7 +168,7 @@ def attention(q, k, v, *, cu_seqlens_q=None, cu_seqlens_k=None, causal: bool = F
     ws, ws_bytes, _keep = _workspace(workspace, nbytes, device)
     _call(device, lib.svdq_attention, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), cu_q, cu_k,
           batch, total_q, total_k, heads_q, heads_k, head_dim, strides,
-          head_dim ** -0.5 if scale is None else float(scale), 1 if causal else 0, code, ws, ws_bytes)
+          (head_dim or 1) ** -0.5 if scale is None else float(scale), 1 if causal else 0, code, ws, ws_bytes)
     return (out, lse) if return_lse else out
 
 
@@ -235,6 +238,8 @@ def linear16(x, w, bias=None, *, activation: str = "none", gate=None, residual=N
     except (AttributeError, ValueError):
         raise TypeError("w: expected a device tensor [N][K]") from None
     _like(w, dtype, device, (N, K), "w")
+    if M > _MOST or N > _MOST:
+        raise ValueError("linear16: more rows than the library counts (2^31 - 2^16)")
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation: expected one of {tuple(ACTIVATIONS)}, got {activation!r}")
@@ -269,6 +274,8 @@ def layer_norm(x, weight=None, bias=None, *, scale=None, shift=None, group_rows=
     code, device = _operand(x, 2, "x", "[M][K]")
     M, K = x.shape
     dtype = x.dtype
+    if M > _MOST:
+        raise ValueError("layer_norm: more rows than the library counts (2^31 - 2^16)")
     if weight is not None:
         _like(weight, dtype, device, (K,), "weight")
     if bias is not None:

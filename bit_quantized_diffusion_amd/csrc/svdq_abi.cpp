@@ -48,24 +48,27 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 int check_dtype(int dtype) { return dtype == SVDQ_BF16 || dtype == SVDQ_F16 ? SVDQ_OK : SVDQ_ERR_INVALID_ARG; }
 
+// rows that the 16-bit operators count: a tile more still fits 31 bits
+constexpr long long kMostRows = (1LL << 31) - (1LL << 16);
+
 int check_attention_shape(int total_q, int total_k, int batch, int heads_q, int heads_k, int head_dim) {
   if (total_q < 0 || total_k < 0 || batch < 1 || heads_q < 1 || heads_k < 1 || heads_q % heads_k) return SVDQ_ERR_SHAPE;
   if (head_dim < 8 || head_dim > 128 || head_dim % 8) return SVDQ_ERR_SHAPE;
-  // the rows of one key head, and the workgroups (32 rows or more each, at
-  // most 64 splits), are counted in 31 bits
+  // the rows of one key head, the keys (each rounded up to a tile) and the
+  // workgroups (32 rows or more each, at most 64 splits) are counted in 31 bits
   const long long rows = static_cast<long long>(total_q) * (heads_q / heads_k);
-  if (rows >= 1LL << 31 || (rows / 32 + batch) * heads_k * 64 >= 1LL << 31) return SVDQ_ERR_SHAPE;
+  if (rows > kMostRows || total_k > kMostRows || (rows / 32 + batch) * heads_k * 64 >= 1LL << 31) return SVDQ_ERR_SHAPE;
   return SVDQ_OK;
 }
 
 bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 
 int check_linear16_shape(int M, int N, int K) {
-  if (M < 1 || N < 1 || K < 1) return SVDQ_ERR_SHAPE;
-  // tiles of 128 x 128 (32 channels for few rows) and 8-channel pieces of
-  // the result are counted in 31 bits
+  if (M < 1 || N < 1 || K < 1 || M > kMostRows || N > kMostRows) return SVDQ_ERR_SHAPE;
+  // tiles of 64 x 64 or more, and workgroups of 256 x 8 channels of the
+  // result, are counted in 31 bits
   const long long m = M, n = N;
-  if (((m + 127) / 128) * ((n + 127) / 128) >= 1LL << 31 || ((n + 7) / 8) * m >= 1LL << 39) return SVDQ_ERR_SHAPE;
+  if (((m + 63) / 64) * ((n + 63) / 64) >= 1LL << 31 || ((n + 7) / 8) * m >= 1LL << 39) return SVDQ_ERR_SHAPE;
   return SVDQ_OK;
 }
 
@@ -343,7 +346,7 @@ int svdq_attention(const void* q, const void* k, const void* v, void* o, float* 
     if (total_k <= 1) own[i] = head_dim;
     if (own[i] < head_dim || own[i] > 1 << 23) return SVDQ_ERR_INVALID_ARG;
   }
-  if (!(scale > 0.f) || std::isinf(scale)) return SVDQ_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || std::isinf(scale * 2.f)) return SVDQ_ERR_INVALID_ARG;
   if ((st = current_device_ok())) return st;
   if (total_q == 0) return SVDQ_OK;
   return hip_status(svdq_launch_attention(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, batch, total_q, total_k, heads_q,
@@ -372,8 +375,10 @@ int svdq_linear16(const void* x, int64_t ldx, const void* w, int64_t ldw, const 
   if (!aligned2(x) || !aligned2(w) || !aligned2(y) || !aligned2(bias) || !aligned2(gate) || !aligned2(residual) ||
       !aligned16(workspace))
     return SVDQ_ERR_INVALID_ARG;
-  constexpr int64_t kMostLd = 1 << 22;
-  if (ldx < K || ldw < K || ldx > kMostLd || ldw > kMostLd || ldy < N || (residual && ldr < N)) return SVDQ_ERR_SHAPE;
+  if (ldx < K || ldw < K || ldy < N || (residual && ldr < N)) return SVDQ_ERR_SHAPE;
+  // a tile's 256 rows are addressed with 31-bit byte offsets
+  const int64_t most_ld = ldx > ldw ? ldx : ldw;
+  if (most_ld > 1 << 22 || 255 * most_ld + K >= 1 << 30) return SVDQ_ERR_SHAPE;
   if (gate && (ld_gate < N || group_rows < 1)) return SVDQ_ERR_SHAPE;
   if ((st = current_device_ok())) return st;
   return hip_status(svdq_launch_linear16(x, ldx, w, ldw, bias, gate, ld_gate, group_rows, residual, ldr, y, ldy, M, N, K,
@@ -389,7 +394,7 @@ int svdq_layer_norm(const void* x, int64_t ldx, const void* weight, const void* 
   if (!aligned2(x) || !aligned2(y) || !aligned2(weight) || !aligned2(bias) || !aligned2(scale) || !aligned2(shift))
     return SVDQ_ERR_INVALID_ARG;
   if (!(eps >= 0.f) || std::isinf(eps)) return SVDQ_ERR_INVALID_ARG;
-  if (M < 1 || K < 1 || K > 65536 || ldx < K || ldy < K) return SVDQ_ERR_SHAPE;
+  if (M < 1 || M > kMostRows || K < 1 || K > 65536 || ldx < K || ldy < K) return SVDQ_ERR_SHAPE;
   if ((scale || shift) && (ld_mod < K || group_rows < 1)) return SVDQ_ERR_SHAPE;
   if ((st = current_device_ok())) return st;
   return hip_status(svdq_launch_layer_norm(x, ldx, weight, bias, scale, shift, ld_mod, group_rows < 1 ? 1 : group_rows, y,

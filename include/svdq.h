@@ -352,13 +352,15 @@ SVDQ_API int svdq_unfused_linear_noalloc(const void* x, int M, int K,
  * that no query of a row's sequence can see, and what lies past a
  * sequence's end, may hold anything; a NaN or infinity in v at a key hidden
  * from a query only by the causal rule can reach that query's o (0 * NaN).
- * head_dim: a multiple of 8, 8 to 128.  total_q, total_k >= 0,
- * total_q (heads_q / heads_k) < 2^31.  scale > 0 and finite.
+ * o overlaps none of q, k and v.
+ * head_dim: a multiple of 8, 8 to 128.  total_q, total_k >= 0; total_k and
+ * total_q (heads_q / heads_k) at most 2^31 - 2^16.  0 < scale < 2^127.
  * workspace (dev, 16-byte aligned): with the bytes that
  * svdq_attention_workspace_size names, calls with few queries (single
- * tokens against long caches) cut each sequence's keys into parts whose
- * results a second kernel joins in a fixed order; with NULL or fewer bytes
- * one workgroup runs through all keys.  Results are deterministic. */
+ * tokens against long caches) cut the keys into parts whose results a second
+ * kernel joins in a fixed order; with NULL or fewer bytes one workgroup runs
+ * through all keys of its queries.  Results are deterministic; the schedule
+ * goes by the sizes passed here, not by the lengths on the device. */
 SVDQ_API int svdq_attention_workspace_size(int total_q, int total_k, int batch, int heads_q,
                               int heads_k, int head_dim, size_t* out_bytes);
 SVDQ_API int svdq_attention(const void* q, const void* k, const void* v, void* o, float* lse,
@@ -382,8 +384,9 @@ SVDQ_API int svdq_attention(const void* q, const void* k, const void* v, void* o
  * applied in fp32 and y is rounded once.  activation: SVDQ_ACT_NONE,
  * SVDQ_ACT_GELU (the tanh form, as in svdq_gemm_w4a4_lora_up_gelu) or
  * SVDQ_ACT_SILU (z / (1 + exp(-z))).
- * M, N, K >= 1, any values; strides in elements, at least the row's length
- * and at most 2^22 for x and w; group_rows >= 1.  Pointers need 2-byte
+ * M, N, K >= 1, M and N at most 2^31 - 2^16; strides in elements, at least
+ * the row's length; those of x and w at most 2^22 with 255 ld + K < 2^30;
+ * group_rows >= 1.  y overlaps neither x nor w.  Pointers need 2-byte
  * alignment only; rows of x and w that are 16-byte aligned with
  * K % 8 == 0 take the faster loads.
  * workspace (dev, 16-byte aligned): with the bytes that
@@ -412,7 +415,7 @@ SVDQ_API int svdq_linear16(const void* x, int64_t ldx, const void* w, int64_t ld
  *   weight, bias   (dev) [K], each or both NULL
  *   scale, shift   (dev) [ceil(M / group_rows)][K], row stride ld_mod >= K,
  *                  each or both NULL
- * M >= 1; K from 1 to 65536; group_rows >= 1; eps >= 0 and finite.  Pointers
+ * 1 <= M <= 2^31 - 2^16; K from 1 to 65536; group_rows >= 1; eps >= 0 and finite.  Pointers
  * need 2-byte alignment only. */
 SVDQ_API int svdq_layer_norm(const void* x, int64_t ldx, const void* weight, const void* bias,
                               const void* scale, const void* shift, int64_t ld_mod, int group_rows,

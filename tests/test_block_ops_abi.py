@@ -45,7 +45,8 @@ def with_stride(i, value):
     (dict(scale=math.nan), BAD), (dict(scale=math.inf), BAD), (dict(dtype=2), BAD),
     (dict(batch=0), SHAPE), (dict(tq=-1), SHAPE), (dict(tk=-1), SHAPE), (dict(hq=0), SHAPE), (dict(hk=3), SHAPE), (dict(hk=0), SHAPE),
     (dict(d=0), SHAPE), (dict(d=60), SHAPE), (dict(d=136), SHAPE), (dict(tq=2 ** 31 - 1, hq=64, hk=2), SHAPE),
-    (dict(tq=2 ** 30, hq=64, hk=64), SHAPE),
+    (dict(tq=2 ** 30, hq=64, hk=64), SHAPE), (dict(tk=2 ** 31 - 100), SHAPE), (dict(tq=2 ** 31 - 100, hq=1, hk=1), SHAPE),
+    (dict(scale=3e38), BAD),
 ])
 def test_attention_refuses(kw, want):
     assert attention(**kw) == want
@@ -76,6 +77,7 @@ NORM = dict(x=FAKE, ldx=64, weight=FAKE, bias=FAKE, scale=FAKE, shift=FAKE, ld=6
     (dict(residual=ctypes.c_void_p(0x10001)), BAD), (dict(ws=MIS), BAD), (dict(act=3), BAD), (dict(dtype=-1), BAD),
     (dict(m=0), SHAPE), (dict(n=0), SHAPE), (dict(k=0), SHAPE), (dict(ldx=63), SHAPE), (dict(ldw=63), SHAPE), (dict(ldy=31), SHAPE),
     (dict(ldr=31), SHAPE), (dict(ld_gate=31), SHAPE), (dict(rows=0), SHAPE), (dict(ldx=(1 << 22) + 1), SHAPE),
+    (dict(k=1 << 22, ldx=1 << 22, ldw=1 << 22), SHAPE), (dict(m=2 ** 31 - 100), SHAPE), (dict(n=2 ** 31 - 100, ldy=2 ** 31, ldr=2 ** 31, ld_gate=2 ** 31), SHAPE),
 ])
 def test_linear16_refuses(kw, want):
     assert bq.lib.svdq_linear16(*dict(LINEAR, **kw).values(), None) == want
@@ -94,7 +96,7 @@ def test_linear16_workspace_size():
     (dict(x=None), BAD), (dict(y=None), BAD), (dict(scale=ctypes.c_void_p(0x10001)), BAD), (dict(eps=-1.0), BAD),
     (dict(eps=math.nan), BAD), (dict(eps=math.inf), BAD), (dict(dtype=5), BAD), (dict(m=0), SHAPE), (dict(k=0), SHAPE),
     (dict(k=65537, ldx=65537, ldy=65537, ld=65537), SHAPE), (dict(ldx=63), SHAPE), (dict(ldy=63), SHAPE), (dict(ld=63), SHAPE),
-    (dict(rows=0), SHAPE),
+    (dict(rows=0), SHAPE), (dict(m=2 ** 31 - 100), SHAPE),
 ])
 def test_layer_norm_refuses(kw, want):
     assert bq.lib.svdq_layer_norm(*dict(NORM, **kw).values(), None) == want
