@@ -54,10 +54,10 @@ constexpr long long kMostRows = (1LL << 31) - (1LL << 16);
 int check_attention_shape(int total_q, int total_k, int batch, int heads_q, int heads_k, int head_dim) {
   if (total_q < 0 || total_k < 0 || batch < 1 || heads_q < 1 || heads_k < 1 || heads_q % heads_k) return SVDQ_ERR_SHAPE;
   if (head_dim < 8 || head_dim > 128 || head_dim % 8) return SVDQ_ERR_SHAPE;
-  // the rows of one key head, the keys (each rounded up to a tile) and the
-  // workgroups (32 rows or more each, at most 64 splits) are counted in 31 bits
+  // the rows of one key head and the keys, each rounded up to a tile, are
+  // counted in 31 bits; a launch holds less than 2^32 threads: 256 for 32 rows
   const long long rows = static_cast<long long>(total_q) * (heads_q / heads_k);
-  if (rows > kMostRows || total_k > kMostRows || (rows / 32 + batch) * heads_k * 64 >= 1LL << 31) return SVDQ_ERR_SHAPE;
+  if (rows > kMostRows || total_k > kMostRows || (rows / 32 + batch) * heads_k >= 1LL << 24) return SVDQ_ERR_SHAPE;
   return SVDQ_OK;
 }
 
@@ -65,10 +65,11 @@ bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0
 
 int check_linear16_shape(int M, int N, int K) {
   if (M < 1 || N < 1 || K < 1 || M > kMostRows || N > kMostRows) return SVDQ_ERR_SHAPE;
-  // tiles of 64 x 64 or more, and workgroups of 256 x 8 channels of the
-  // result, are counted in 31 bits
+  // a launch holds less than 2^32 threads: 256 for a tile of 64 x 64 or more,
+  // for 32 channels of few rows, or for 8 channels of a row of the splits' sum
+  // (of fewer than 512 tiles)
   const long long m = M, n = N;
-  if (((m + 63) / 64) * ((n + 63) / 64) >= 1LL << 31 || ((n + 7) / 8) * m >= 1LL << 39) return SVDQ_ERR_SHAPE;
+  if (((m + 63) / 64) * ((n + 63) / 64) >= 1LL << 24 || (n + 31) / 32 >= 1LL << 24) return SVDQ_ERR_SHAPE;
   return SVDQ_OK;
 }
 

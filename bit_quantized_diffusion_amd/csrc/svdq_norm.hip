@@ -68,6 +68,10 @@ __device__ __forceinline__ v4u row_chunk(const uint16_t* p, int k, int K) {
   return v;
 }
 
+// workgroups along x, the others along y: one axis of a launch holds less
+// than 2^32 threads
+constexpr unsigned kGridX = 1u << 21;
+
 // CHUNKS chunks of 8 values a lane
 template <typename E, int LANES, int WAVES, int CHUNKS, bool TAIL>
 __global__ __launch_bounds__(WAVES > 1 ? WAVES * 64 : 256) void k_layer_norm(NormArgs a) {
@@ -76,7 +80,7 @@ __global__ __launch_bounds__(WAVES > 1 ? WAVES * 64 : 256) void k_layer_norm(Nor
   constexpr int kRows = WAVES > 1 ? 1 : 256 / LANES;       // rows of a workgroup
   __shared__ float sums[2][WAVES];
   const int t = threadIdx.x % kThreads;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kThreads;
+  const int64_t row = (static_cast<int64_t>(blockIdx.y) * kGridX + blockIdx.x) * kRows + threadIdx.x / kThreads;
   if (row >= a.M) return;   // whole rows' lanes leave together
   const uint16_t* const x = a.x + row * a.ldx;
   v4u raw[CHUNKS];
@@ -144,11 +148,12 @@ template <typename E, int LANES, int WAVES, int CHUNKS>
 void start(const NormArgs& a, hipStream_t stream) {
   constexpr int kRows = WAVES > 1 ? 1 : 256 / LANES;
   const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(a.M) + kRows - 1) / kRows);
+  const dim3 grid(blocks < kGridX ? blocks : kGridX, (blocks + kGridX - 1) / kGridX);
   constexpr int kBlock = WAVES > 1 ? WAVES * 64 : 256;
   if (a.K % 8)
-    k_layer_norm<E, LANES, WAVES, CHUNKS, true><<<blocks, kBlock, 0, stream>>>(a);
+    k_layer_norm<E, LANES, WAVES, CHUNKS, true><<<grid, kBlock, 0, stream>>>(a);
   else
-    k_layer_norm<E, LANES, WAVES, CHUNKS, false><<<blocks, kBlock, 0, stream>>>(a);
+    k_layer_norm<E, LANES, WAVES, CHUNKS, false><<<grid, kBlock, 0, stream>>>(a);
 }
 
 template <typename E>

@@ -354,7 +354,8 @@ SVDQ_API int svdq_unfused_linear_noalloc(const void* x, int M, int K,
  * from a query only by the causal rule can reach that query's o (0 * NaN).
  * o overlaps none of q, k and v.
  * head_dim: a multiple of 8, 8 to 128.  total_q, total_k >= 0; total_k and
- * total_q (heads_q / heads_k) at most 2^31 - 2^16.  0 < scale < 2^127.
+ * rows = total_q (heads_q / heads_k) at most 2^31 - 2^16, and
+ * (rows / 32 + batch) heads_k below 2^24.  0 < scale < 2^127.
  * workspace (dev, 16-byte aligned): with the bytes that
  * svdq_attention_workspace_size names, calls with few queries (single
  * tokens against long caches) cut the keys into parts whose results a second
@@ -384,7 +385,8 @@ SVDQ_API int svdq_attention(const void* q, const void* k, const void* v, void* o
  * applied in fp32 and y is rounded once.  activation: SVDQ_ACT_NONE,
  * SVDQ_ACT_GELU (the tanh form, as in svdq_gemm_w4a4_lora_up_gelu) or
  * SVDQ_ACT_SILU (z / (1 + exp(-z))).
- * M, N, K >= 1, M and N at most 2^31 - 2^16; strides in elements, at least
+ * M, N, K >= 1, M at most 2^31 - 2^16, N at most 2^29 - 32, fewer than 2^24
+ * tiles of 64 x 64 in the result; strides in elements, at least
  * the row's length; those of x and w at most 2^22 with 255 ld + K < 2^30;
  * group_rows >= 1.  y overlaps neither x nor w.  Pointers need 2-byte
  * alignment only; rows of x and w that are 16-byte aligned with

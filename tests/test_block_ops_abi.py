@@ -46,7 +46,7 @@ def with_stride(i, value):
     (dict(batch=0), SHAPE), (dict(tq=-1), SHAPE), (dict(tk=-1), SHAPE), (dict(hq=0), SHAPE), (dict(hk=3), SHAPE), (dict(hk=0), SHAPE),
     (dict(d=0), SHAPE), (dict(d=60), SHAPE), (dict(d=136), SHAPE), (dict(tq=2 ** 31 - 1, hq=64, hk=2), SHAPE),
     (dict(tq=2 ** 30, hq=64, hk=64), SHAPE), (dict(tk=2 ** 31 - 100), SHAPE), (dict(tq=2 ** 31 - 100, hq=1, hk=1), SHAPE),
-    (dict(scale=3e38), BAD),
+    (dict(scale=3e38), BAD), (dict(tq=2 ** 29, hq=1, hk=1), SHAPE), (dict(batch=2 ** 24), SHAPE),
 ])
 def test_attention_refuses(kw, want):
     assert attention(**kw) == want
@@ -78,6 +78,7 @@ NORM = dict(x=FAKE, ldx=64, weight=FAKE, bias=FAKE, scale=FAKE, shift=FAKE, ld=6
     (dict(m=0), SHAPE), (dict(n=0), SHAPE), (dict(k=0), SHAPE), (dict(ldx=63), SHAPE), (dict(ldw=63), SHAPE), (dict(ldy=31), SHAPE),
     (dict(ldr=31), SHAPE), (dict(ld_gate=31), SHAPE), (dict(rows=0), SHAPE), (dict(ldx=(1 << 22) + 1), SHAPE),
     (dict(k=1 << 22, ldx=1 << 22, ldw=1 << 22), SHAPE), (dict(m=2 ** 31 - 100), SHAPE), (dict(n=2 ** 31 - 100, ldy=2 ** 31, ldr=2 ** 31, ld_gate=2 ** 31), SHAPE),
+    (dict(n=2 ** 29, ldy=2 ** 29, ldr=2 ** 29, ld_gate=2 ** 29), SHAPE), (dict(m=2 ** 29, n=128, ldy=128, ldr=128, ld_gate=128), SHAPE),
 ])
 def test_linear16_refuses(kw, want):
     assert bq.lib.svdq_linear16(*dict(LINEAR, **kw).values(), None) == want

@@ -144,3 +144,18 @@ def test_wrapper_refuses():
         bq.layer_norm(x, eps=-1.0)
     with pytest.raises(bq.SvdqError):
         bq.layer_norm(torch.zeros(1, 65537, device="cuda", dtype=BF))
+
+
+def test_more_rows_than_one_axis_of_a_launch():
+    m, k = 2 ** 29 + 5, 8   # 8 lanes a row: past 2^32 threads, and past 2^32 elements
+    g = torch.Generator().manual_seed(8)
+    part = torch.randn(2 ** 20, k, generator=g).to(BF).cuda()
+    x = torch.empty(m, k, dtype=BF, device="cuda")
+    x[:2 ** 29].view(2 ** 9, 2 ** 20, k).copy_(part.expand(2 ** 9, -1, -1))
+    x[2 ** 29:] = part[:5]
+    y = bq.layer_norm(x, out=x)
+    torch.cuda.synchronize()
+    want, bound = layer_norm_reference(part, None, None, None, None, 1, 1e-6)
+    for first in (0, 2 ** 20, 2 ** 24 - 2 ** 20, 2 ** 28, 2 ** 29 - 2 ** 20):
+        assert_within(y[first:first + 2 ** 20], want, bound, f"rows from {first}")
+    assert_within(y[2 ** 29:], want[:5], bound[:5] if torch.is_tensor(bound) else bound, "last rows")
