@@ -150,7 +150,7 @@ def attention(q, k, v, *, cu_seqlens_q=None, cu_seqlens_k=None, causal: bool = F
         cu_q, cu_k = cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr()
     sq, sk, sv, so = q.stride(), k.stride(), v.stride(), (heads_q * head_dim, head_dim)
     if out is None:
-        out = q.new_empty((total_q, heads_q, head_dim))
+        out = q.new_empty(total_q, heads_q, head_dim)
     else:
         _like(out, dtype, device, q.shape, "out")
         so = out.stride()
@@ -250,7 +250,7 @@ def linear16(x, w, bias=None, *, activation: str = "none", gate=None, residual=N
     if residual is not None:
         _like(residual, dtype, device, (M, N), "residual")
     if out is None:
-        out = x.new_empty((M, N))
+        out = x.new_empty(M, N)
     else:
         _like(out, dtype, device, (M, N), "out")
     if M == 0:
@@ -290,7 +290,7 @@ def layer_norm(x, weight=None, bias=None, *, scale=None, shift=None, group_rows=
             raise ValueError("scale and shift must have the same groups and row stride")
         rows, ld = shift_rows, ld_shift
     if out is None:
-        out = x.new_empty((M, K))
+        out = x.new_empty(M, K)
     else:
         _like(out, dtype, device, (M, K), "out")
     if M == 0:
