@@ -1,4 +1,5 @@
-"""Build libsvdq.so in-tree with hipcc for gfx950.
+"""Build libsvdq.so in-tree with hipcc for gfx950, and _block_ops.so, the
+Python side of the 16-bit block operators.
 
     python bit_quantized_diffusion_amd/build.py [-v]
 
@@ -18,11 +19,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsvdq.so")
+PYTHON_LIB = os.path.join(PKG, "_block_ops.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")
 CLANGXX = os.path.join(ROCM, "llvm", "bin", "clang++")
@@ -38,6 +41,7 @@ HOST_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-pthread",
 
 KERNEL_SOURCES = ["svdq_kernels.hip", "svdq_attention.hip", "svdq_linear16.hip", "svdq_norm.hip"]
 HOST_SOURCES = ["svdq_abi.cpp", "svdq_pack.cpp"]
+PYTHON_SOURCE = "svdq_python.cpp"
 
 
 def _run(cmd, verbose):
@@ -56,7 +60,8 @@ def _run(cmd, verbose):
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libsvdq.so; returns the library path."""
+    """Compile every source and link both libraries; returns the path of
+    libsvdq.so."""
     tmp = tempfile.mkdtemp(prefix="svdq_build_")
     try:
         objs = []
@@ -68,6 +73,9 @@ def build(verbose: bool = False) -> str:
         for src in HOST_SOURCES:
             obj = os.path.join(tmp, src + ".o")
             procs.append(([compiler, "-x", "c++", *HOST_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj], obj))
+        python_obj = os.path.join(tmp, PYTHON_SOURCE + ".o")
+        procs.append(([compiler, "-x", "c++", *HOST_FLAGS, f"-I{sysconfig.get_paths()['include']}", "-c",
+                       os.path.join(CSRC, PYTHON_SOURCE), "-o", python_obj], python_obj))
         running = [(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True), cmd, obj)
                    for cmd, obj in procs]
         for p, cmd, obj in running:
@@ -77,12 +85,18 @@ def build(verbose: bool = False) -> str:
                 raise RuntimeError(f"build step failed: {' '.join(cmd)}")
             if verbose:
                 print(" ".join(cmd), flush=True)
-            objs.append(obj)
+            if obj != python_obj:
+                objs.append(obj)
         tmp_lib = os.path.join(tmp, "libsvdq.so")
         _run([HIPCC, "-shared", f"--offload-arch={ARCH}", "-fPIC", "-pthread", "-o", tmp_lib, *objs], verbose)
-        staged = LIB + ".tmp"
-        shutil.copyfile(tmp_lib, staged)
-        os.replace(staged, LIB)
+        # finds libsvdq.so beside itself
+        tmp_python = os.path.join(tmp, "_block_ops.so")
+        _run([compiler, "-shared", "-o", tmp_python, python_obj, f"-L{tmp}", "-l:libsvdq.so", "-Wl,-rpath,$ORIGIN"],
+             verbose)
+        for built, path in ((tmp_lib, LIB), (tmp_python, PYTHON_LIB)):
+            staged = path + ".tmp"
+            shutil.copyfile(built, staged)
+            os.replace(staged, path)
         return LIB
     finally:
         shutil.rmtree(tmp, ignore_errors=True)
