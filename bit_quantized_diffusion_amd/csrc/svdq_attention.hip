@@ -699,6 +699,12 @@ __global__ __launch_bounds__(256, 1) void k_attention_few(AttnArgs a) {
 // results share one).
 constexpr int kSpreadBatch = 512;
 
+// Units of a tile of rows on the line: its tiles of keys, and before them
+// what starting it costs a workgroup (5 tokens of 24 heads over 1342, 124, 14,
+// 4 and 1 keys: 28 us with the tiles alone, 17 with these).
+constexpr int kStartUnits = 8;
+__device__ __forceinline__ int line_units(int len_k) { return len_k > 0 ? ((len_k + 31) >> 5) + kStartUnits : 0; }
+
 template <typename E, int DP>
 __global__ __launch_bounds__(256, 1) void k_attention_spread(AttnArgs a) {
   using F = Few<E, DP>;
@@ -715,7 +721,7 @@ __global__ __launch_bounds__(256, 1) void k_attention_spread(AttnArgs a) {
       if (i0 + lane < a.batch) {
         const Tile t = sequence(a, i0 + lane);
         nq = (t.rows + 31) >> 5;
-        n = static_cast<int64_t>(nq) * ((t.len_k + 31) >> 5);
+        n = static_cast<int64_t>(nq) * line_units(t.len_k);
       }
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
@@ -753,18 +759,19 @@ __global__ __launch_bounds__(256, 1) void k_attention_spread(AttnArgs a) {
     const int64_t r = at - head * per_head;
     const int seq = last_before(a.batch, [&](int i) { return before[i] <= r; });
     Tile t = sequence(a, seq);
-    const int tiles_k = (t.len_k + 31) >> 5;
-    const int rest = static_cast<int>(r - before[seq]);
-    const int qt = rest / tiles_k, k0 = rest - qt * tiles_k;
-    const int k1 = static_cast<int>(end - at < tiles_k - k0 ? k0 + (end - at) : tiles_k);
+    const int units = line_units(t.len_k);
+    const int64_t rest = r - before[seq];
+    const int qt = static_cast<int>(rest / units), u0 = static_cast<int>(rest - static_cast<int64_t>(qt) * units);
+    const int u1 = static_cast<int>(end - at < units - u0 ? u0 + (end - at) : units);
+    at += u1 - u0;
+    if (u1 <= kStartUnits) continue;   // its first tile of keys is the next workgroup's
     t.row0 = qt * 32;
     const int64_t p = static_cast<int64_t>(blockIdx.x) + static_cast<int64_t>(head) * tiles_q + before_q[seq] + qt;
     if (p >= a.results) return;   // only with starts that do not rise
-    F::run(a, t, head, k0, k1, lds);
+    F::run(a, t, head, u0 > kStartUnits ? u0 - kStartUnits : 0, u1 - kStartUnits, lds);
     F::finish(
         a, t, lds, [&](int row, float m, float l) { a.part_ml[p * 32 + row] = make_float2(m, l); },
         [&](int row, int d, v4f x, float) { *reinterpret_cast<v4f*>(a.part_o + (p * 32 + row) * a.D + d) = x; });
-    at += k1 - k0;
     __syncthreads();   // LDS is read out before the next loads
   }
 }
@@ -788,7 +795,7 @@ __global__ __launch_bounds__(256) void k_attention_spread_join(AttnArgs a) {
   int n = 0;   // workgroups from the first to the last that took part
   int64_t first = 0, b0 = 0, b1 = 0, tile = 0;
   if (tiles_k > 0 && row >= 0 && row < t.rows) {
-    b0 = head * per_head + a.before[seq] + static_cast<int64_t>(qt) * tiles_k;
+    b0 = head * per_head + a.before[seq] + static_cast<int64_t>(qt) * line_units(t.len_k) + kStartUnits;
     b1 = b0 + tiles_k;
     // workgroup w begins at floor(total w / spread)
     first = ((b0 + 1) * a.spread - 1) / total;
@@ -908,9 +915,16 @@ Plan plan_for(int total_q, int total_k, int batch, int heads_q, int heads_k, int
   p.bytes = 0;
   const int64_t n = units(p.waves ? p.waves * 32 : 32);
   if (p.waves == 0) {
-    // Where the tiles of rows would not give every CU two workgroups, one
-    // workgroup a CU with equal shares of at least 8 tiles of keys, two a wave.
-    int64_t w = n / heads_k * ((mean_keys + 31) / 32) * heads_k / 8;
+    // Where the tiles of rows would not give every CU two workgroups and the
+    // keys are long, one workgroup a CU with equal shares of at least 12 units.
+    // One token over so many keys, in one workgroup a head and spread, the
+    // second kernel with it (24 heads of 128): 300 keys 8 and 14 us, 1000 keys
+    // 15 and 15, 2000 keys 24 and 16, 4000 keys 54 and 22.  Of several
+    // sequences the mean alone is known but the longest counts: from 256 keys
+    // (4 of 300 each 8 and 14 us, 5 of 1342 .. 1 18 and 17).
+    const int64_t tiles = (mean_keys + 31) / 32;
+    if (tiles <= (batch == 1 ? 32 : 8)) return p;
+    int64_t w = n / heads_k * (tiles + kStartUnits) * heads_k / 12;
     if (w > 256) w = 256;
     if (n >= 512 || batch > kSpreadBatch || w <= n) return p;
     p.spread = static_cast<int>(w);
@@ -918,7 +932,11 @@ Plan plan_for(int total_q, int total_k, int batch, int heads_q, int heads_k, int
     p.bytes = spread_head(batch) + static_cast<size_t>(results) * 32 * (D + 2) * 4;
     return p;
   }
-  int64_t s = n >= 128 ? 1 : (256 + n - 1) / n;
+  // Splits: where the tiles would leave half the CUs idle; and in two where
+  // they would give a CU one workgroup at most and the keys are long (4 heads
+  // of 128 over 4096 and 8192 keys 66 -> 54 and 190 -> 143 us, causal 66 -> 48
+  // and 127 -> 100; 8 heads over 2048 keys 37 -> 45).
+  int64_t s = n < 128 ? (256 + n - 1) / n : p.waves == 4 && n <= 256 && mean_keys >= 4096 ? 2 : 1;
   if (s > mean_keys / 512) s = mean_keys / 512;
   p.splits = static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
   if (p.splits > 1) p.bytes = static_cast<size_t>(p.splits) * total_q * heads_q * (D + 2) * 4;

@@ -142,6 +142,30 @@ def test_equal_shares_of_the_keys(lens_q, lens_k, hq, hk, d):
         assert torch.equal(a, b) and torch.equal(la, lb)
 
 
+@pytest.mark.parametrize("lens_q,lens_k,hq,hk,d", [
+    ([1, 2, 2, 1, 1], [1342, 1, 4, 124, 2100], 6, 6, 128),       # parts over several sequences, short ones among them
+    ([1] * 40, [1, 0, 3, 40, 4000] * 8, 4, 2, 96),
+    ([33, 0, 64, 1], [700, 50, 1, 2900], 2, 1, 64),              # tiles of rows of a few tiles of keys
+    ([1], [1025], 1, 1, 8),
+])
+def test_shares_that_end_where_a_tile_of_rows_starts(lens_q, lens_k, hq, hk, d):
+    assert bq.attention_workspace_size(sum(lens_q), sum(lens_k), len(lens_q), hq, hk, d) > 0
+    for seed in (1, 2):
+        q, k, v = inputs(lens_q, lens_k, hq, hk, d, HF, seed)
+        for causal in (False, True):
+            check(q, k, v, lens_q, lens_k, causal, "shares")
+            check(q, k, v, lens_q, lens_k, causal, "whole", workspace=None)
+
+
+def test_long_keys_and_few_heads():
+    """One workgroup a CU at most: the keys are cut in two."""
+    for lens_q, lens_k, hq, hk in (([4100], [4200], 4, 4), ([2100, 4001], [8000, 300], 2, 2)):
+        assert bq.attention_workspace_size(sum(lens_q), sum(lens_k), len(lens_q), hq, hk, 40) > 0
+        q, k, v = inputs(lens_q, lens_k, hq, hk, 40, BF, 9)
+        for causal in (False, True):
+            check(q, k, v, lens_q, lens_k, causal, "cut in two")
+
+
 def test_split_with_many_rows():
     """A grid of wide tiles that would leave the device idle is cut along the
     keys as well."""
