@@ -164,8 +164,12 @@ __device__ __forceinline__ void store8(uint16_t* p, v4u v, int count) {
   for (int e = 0; e < 7; ++e)
     if (e < count) p[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
 }
-// the same, not kept in the caches on its way (results that the kernel does
-// not read again)
+// The same, not kept in the caches on its way (results that the kernel does
+// not read again).  On large results, passes over changing inputs: attention
+// 254 -> 246 us (4608 x 24 heads), linear 81 -> 73 (4608 x 3072 x 3072), norm
+// 15.7 -> 14.4 (4608 x 3072).  In a transformer block with the quantized layers
+// no difference (4608 x 3072: 1134 and 1142, 6144 x 1536: 617 and 608 us); two
+// 16-bit linears in a row, 4608 x 3072 x 12288 x 3072, 578 -> 600.
 __device__ __forceinline__ void stream8(uint16_t* p, v4u v) {
   typedef unsigned v4u_any __attribute__((ext_vector_type(4), aligned(2)));
   __builtin_nontemporal_store(v, reinterpret_cast<v4u_any*>(p));

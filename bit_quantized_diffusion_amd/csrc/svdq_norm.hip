@@ -7,8 +7,10 @@
 // Memory-bound: x is read once and y written once, with the row held in
 // registers between (16 bytes a lane and chunk).  The variance is that of
 // the deviations from the mean, a second sum over the registers: rows far
-// off centre lose nothing.  A row belongs to LANES lanes of a wave (rows of
-// up to 4096 values) or to WAVES whole waves that join their sums in LDS.
+// off centre lose nothing.  4608 x 3072 with scale and shift: 14.4 us, 12.2
+// alone (4.6 TB/s; a copy of the same bytes 12.6).  A row belongs to LANES
+// lanes of a wave (rows of up to 4096 values) or to WAVES whole waves that
+// join their sums in LDS.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -136,7 +138,7 @@ __global__ __launch_bounds__(WAVES > 1 ? WAVES * 64 : 256) void k_layer_norm(Nor
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[c][e] += w[e];
     }
-    // streamed: y is not read again here (4608 x 3072: 15 -> 12 us)
+    // streamed: y is not read again here
     if (!TAIL || k + 8 <= a.K)
       stream8(y + k, pack8<E>(f[c]));
     else

@@ -4,8 +4,9 @@
 // The smallest calls take longer on the host than on the device.  With the
 // same checks in Python and a ctypes call one of 77 tokens x 12 heads took 9.6
 // us (attention), of 1 x 256 x 3072 8.9 (linear16) and of 1 x 768 8.1 (layer
-// norm); so they take 6.8, 6.2 and 6.2, of which the launch is 3.6.  Tensors are seen through their Python methods
-// (dtype, get_device, shape, stride, data_ptr, new_empty) alone.
+// norm); so they take 6.8, 6.2 and 6.2, of which the launch is 3.6.  Tensors
+// are seen through their Python methods (dtype, get_device, shape, stride,
+// data_ptr, new_empty) alone.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <math.h>
