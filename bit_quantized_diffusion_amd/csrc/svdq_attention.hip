@@ -89,22 +89,24 @@ __device__ __forceinline__ int last_before(int n, F before) {
   return __builtin_amdgcn_readfirstlane(at);
 }
 
-// Sequence seq's tokens, inside the tensors whatever the starts hold.
-__device__ __forceinline__ Tile sequence(const AttnArgs& a, int seq) {
+// The tokens from the starts q to q1 and k to k1, inside the tensors whatever
+// the starts hold.
+__device__ __forceinline__ Tile between(const AttnArgs& a, int q, int q1, int k, int k1) {
   Tile t;
-  t.q0 = t.k0 = 0;
-  t.len_q = a.total_q;
-  t.len_k = a.total_k;
-  if (a.cu_q) {
-    t.q0 = min(max(a.cu_q[seq], 0), a.total_q);
-    t.len_q = min(max(a.cu_q[seq + 1], t.q0), a.total_q) - t.q0;
-    t.k0 = min(max(a.cu_k[seq], 0), a.total_k);
-    t.len_k = min(max(a.cu_k[seq + 1], t.k0), a.total_k) - t.k0;
-  }
+  t.q0 = min(max(q, 0), a.total_q);
+  t.len_q = min(max(q1, t.q0), a.total_q) - t.q0;
+  t.k0 = min(max(k, 0), a.total_k);
+  t.len_k = min(max(k1, t.k0), a.total_k) - t.k0;
   t.rows = t.len_q * a.group;
   t.row0 = 0;
   t.any = t.rows > 0;
   return t;
+}
+
+// Sequence seq's tokens.
+__device__ __forceinline__ Tile sequence(const AttnArgs& a, int seq) {
+  if (!a.cu_q) return between(a, 0, a.total_q, 0, a.total_k);
+  return between(a, a.cu_q[seq], a.cu_q[seq + 1], a.cu_k[seq], a.cu_k[seq + 1]);
 }
 
 // Rows are cut into tiles of BM per sequence.  Sequence i owns the slots
@@ -113,12 +115,24 @@ __device__ __forceinline__ Tile sequence(const AttnArgs& a, int seq) {
 // slots left over exit.
 template <int BM>
 __device__ __forceinline__ Tile find_tile(const AttnArgs& a, int slot) {
+  // is sequence i's first slot, with its start, at or before this one?
+  auto before = [&](int i, int start) {
+    return static_cast<int64_t>(min(max(start, 0), a.total_q)) * a.group / BM + i <= slot;
+  };
   int seq = 0;
-  if (a.batch > 1)
-    seq = last_before(a.batch, [&](int i) {
-      return static_cast<int64_t>(min(max(a.cu_q[i], 0), a.total_q)) * a.group / BM + i <= slot;
-    });
-  Tile t = sequence(a, seq);
+  Tile t;
+  if (a.batch > 1 && a.batch < 64) {
+    // every start is in the wave: no second way to memory for the sequence's
+    const int i = min(static_cast<int>(threadIdx.x & 63), a.batch);
+    const int q = a.cu_q[i], k = a.cu_k[i];
+    const uint64_t held = __ballot(i < a.batch && before(i, q));
+    seq = max(static_cast<int>(__popcll(held)), 1) - 1;
+    auto of = [](int v, int lane) { return __builtin_amdgcn_readlane(v, lane); };
+    t = between(a, of(q, seq), of(q, seq + 1), of(k, seq), of(k, seq + 1));
+  } else {
+    if (a.batch > 1) seq = last_before(a.batch, [&](int i) { return before(i, a.cu_q[i]); });
+    t = sequence(a, seq);
+  }
   const int64_t first = static_cast<int64_t>(t.q0) * a.group / BM + seq;
   const int64_t row0 = (slot - first) * BM;
   t.any = slot >= first && row0 < t.rows;
@@ -791,22 +805,45 @@ __global__ __launch_bounds__(256) void k_attention_spread_join(AttnArgs a) {
   __shared__ v2f part[4][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int token = blockIdx.x / a.heads_q, hq = blockIdx.x - token * a.heads_q;
-  int seq = 0;
-  if (a.batch > 1) seq = last_before(a.batch, [&](int i) { return a.cu_q[i] <= token; });
-  const Tile t = sequence(a, seq);
-  const int64_t per_head = a.before[a.batch], total = per_head * a.heads_k;
+  int seq = 0, tiles_before, tiles_q;   // tiles of rows
+  int64_t units_before, per_head;       // units of the line
+  Tile t;
+  if (a.batch < 64) {
+    // all of it in one way to memory
+    const int i = min(lane, a.batch);
+    const int64_t units = a.before[i];
+    const int rows = a.before_q[i];
+    int q = i ? a.total_q : 0, k = i ? a.total_k : 0;
+    if (a.cu_q) q = a.cu_q[i], k = a.cu_k[i];
+    const uint64_t held = __ballot(i < a.batch && q <= token);
+    seq = max(static_cast<int>(__popcll(held)), 1) - 1;
+    auto of = [](int v, int from) { return __builtin_amdgcn_readlane(v, from); };
+    auto of64 = [&](int64_t v, int from) {
+      return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(of(static_cast<int>(v >> 32), from))) << 32 |
+                                  static_cast<uint32_t>(of(static_cast<int>(v), from)));
+    };
+    t = between(a, of(q, seq), of(q, seq + 1), of(k, seq), of(k, seq + 1));
+    units_before = of64(units, seq), per_head = of64(units, a.batch);
+    tiles_before = of(rows, seq), tiles_q = of(rows, a.batch);
+  } else {
+    seq = last_before(a.batch, [&](int i) { return a.cu_q[i] <= token; });
+    t = sequence(a, seq);
+    units_before = a.before[seq], per_head = a.before[a.batch];
+    tiles_before = a.before_q[seq], tiles_q = a.before_q[a.batch];
+  }
+  const int64_t total = per_head * a.heads_k;
   const int head = hq / a.group, tiles_k = (t.len_k + 31) >> 5;
   const int row = (token - t.q0) * a.group + hq - head * a.group;
   const int qt = row >> 5;
   int n = 0;   // workgroups from the first to the last that took part
   int64_t first = 0, b0 = 0, b1 = 0, tile = 0;
   if (tiles_k > 0 && row >= 0 && row < t.rows) {
-    b0 = head * per_head + a.before[seq] + static_cast<int64_t>(qt) * line_units(t.len_k) + kStartUnits;
+    b0 = head * per_head + units_before + static_cast<int64_t>(qt) * line_units(t.len_k) + kStartUnits;
     b1 = b0 + tiles_k;
     // workgroup w begins at floor(total w / spread)
     first = ((b0 + 1) * a.spread - 1) / total;
     n = static_cast<int>((b1 * a.spread - 1) / total - first) + 1;
-    tile = static_cast<int64_t>(head) * a.before_q[a.batch] + a.before_q[seq] + qt;
+    tile = static_cast<int64_t>(head) * tiles_q + tiles_before + qt;
   }
   // one result a thread (no more workgroups than threads)
   float2 ml = make_float2(-INFINITY, 0.f);
