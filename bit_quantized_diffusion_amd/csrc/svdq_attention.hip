@@ -327,24 +327,29 @@ __device__ __forceinline__ Job job_of(const AttnArgs& a, int id) {
 // iterations ahead: K of tile i + 2 + kLead and V of tile i + kLead, through
 // rings of slots, with one barrier an iteration.  Products of 32 x 32 x 16: the
 // vector work needs the issue slots that twice as many of 16 x 16 x 32 take.
+//
+// PARTS == 2: as many waves again take the second half of the keys, through
+// rings of their own, and the first half's join the two results at the end.
 // ---------------------------------------------------------------------------
 
-template <typename E, int DP, int NW>
-__global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
+template <typename E, int DP, int NW, int PARTS>
+__global__ __launch_bounds__(PARTS * NW * 64, 2) void k_attention(AttnArgs a) {
   constexpr int kKeys = 64, BM = NW * 32;
   using W = WaveTile<E, DP, kKeys>;
   constexpr int kBuf = W::kBytes;
   constexpr int kLoads = kBuf / 1024 / NW;   // 1 KB loads per wave and operand tile
   // tiles ahead of the ones in use; with 4 waves two workgroups share a CU's LDS
   constexpr int kLead = NW == 8 ? 2 : 1, kSlotsK = 2 + kLead, kSlotsV = 1 + kLead;
-  static_assert(kLoads >= 1 && NW * 32 * DP * 2 <= (kSlotsK + kSlotsV) * kBuf, "loads divide evenly; the output staging fits");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[(kSlotsK + kSlotsV) * kBuf];
+  constexpr int kPart = (kSlotsK + kSlotsV) * kBuf;   // LDS of a part
+  static_assert(kLoads >= 1 && NW * 32 * DP * 2 <= kPart, "loads divide evenly; the output staging fits");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[PARTS * kPart];
 
   const Job job = job_of(a, blockIdx.x);
   const Tile t = find_tile<BM>(a, job.slot);
   if (!t.any) return;
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % NW;
+  const int part = PARTS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / NW : 0;
 
   // this lane's row
   const int row = t.row0 + wave * 32 + l32;
@@ -363,8 +368,9 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
   const int end = a.causal ? min(t.len_k, last_row / a.group + shift) : t.len_k;
   const int tiles = (max(end, 0) + kKeys - 1) / kKeys;
   const int first_lim = a.causal ? min(t.len_k, t.row0 / a.group + shift) : t.len_k;
-  const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * job.split / a.splits);
-  const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (job.split + 1) / a.splits);
+  const int cuts = a.splits * PARTS, cut = job.split * PARTS;
+  auto cut_at = [&](int i) { return static_cast<int>(static_cast<int64_t>(tiles) * i / cuts); };
+  const int t0 = cut_at(cut + part), t1 = cut_at(cut + part + 1);
   const int open = min(max(first_lim, 0) / kKeys, t1);
 
   int kv[kLoads], vv[kLoads];
@@ -373,7 +379,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
     kv[n] = tile_voff<DP, false>(wave * kLoads + n, lane, a.k_t, a.D);
     vv[n] = tile_voff<DP, true>(wave * kLoads + n, lane, a.v_t, a.D);
   }
-  const uint32_t base = lds_addr(lds);
+  const uint32_t base = lds_addr(lds) + part * kPart;
   const uint32_t dst = base + wave * kLoads * 1024;
   const uint16_t* const kp = a.k + t.k0 * a.k_t + job.head * a.k_h;
   const uint16_t* const vp = a.v + t.k0 * a.v_t + job.head * a.v_h;
@@ -519,7 +525,44 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attention(AttnArgs a) {
     iterate(i, s0, s1, No{}, No{});
   }
 
-  const float l = w.row_sum();
+  float l = w.row_sum();
+  if constexpr (PARTS > 1) {
+    // every part meets the barriers of the longest: two and one a tile
+    static_assert(PARTS == 2, "the join is written for two");
+    const int mine = t1 > t0 ? 2 + t1 - t0 : 0;
+    const int other = cut_at(cut + 2 - part) - cut_at(cut + 1 - part);
+    const int all = max(mine, other > 0 ? 2 + other : 0);
+    for (int i = mine; i < all; ++i) lds_wait_barrier<0>();
+    // the second part's O, m and l through its LDS, a lane's for the same lane
+    constexpr int kQuads = W::kDt * 4;
+    static_assert((kQuads * 16 + 8) * 64 * NW <= kPart, "the join fits");
+    uint8_t* const joint = lds + kPart + wave * (kQuads * 16 + 8) * 64;
+    if (part == 1) {
+#pragma unroll
+      for (int d = 0; d < W::kDt; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<v4f*>(joint + ((d * 4 + j) * 64 + lane) * 16) =
+              v4f{w.acc[d][4 * j], w.acc[d][4 * j + 1], w.acc[d][4 * j + 2], w.acc[d][4 * j + 3]};
+      *reinterpret_cast<v2f*>(joint + kQuads * 1024 + lane * 8) = v2f{w.m, l};
+    }
+    __syncthreads();
+    if (part == 1) return;
+    const v2f ml = *reinterpret_cast<const v2f*>(joint + kQuads * 1024 + lane * 8);
+    const float m = ml[0] > w.m ? ml[0] : w.m;
+    const float f0 = w.m == -INFINITY ? 0.f : exp2_fast((w.m - m) * w.sc);
+    const float f1 = ml[0] == -INFINITY ? 0.f : exp2_fast((ml[0] - m) * w.sc);
+    w.m = m;
+    l = l * f0 + ml[1] * f1;
+#pragma unroll
+    for (int d = 0; d < W::kDt; ++d)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const v4f x = *reinterpret_cast<const v4f*>(joint + ((d * 4 + j) * 64 + lane) * 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w.acc[d][4 * j + e] = w.acc[d][4 * j + e] * f0 + x[e] * f1;
+      }
+  }
   const int64_t out_row = static_cast<int64_t>(t.q0 + token) * a.heads_q + head;
   if (a.splits > 1) {
     if (valid) {
@@ -930,6 +973,7 @@ __global__ __launch_bounds__(256) void k_attention_join(AttnArgs a) {
 struct Plan {
   int waves;     // rows a workgroup takes / 32; 0: k_attention_few or k_attention_spread
   int splits;    // of a tile's keys, waves > 0
+  int parts;     // of the keys within a workgroup, waves == 4
   int spread;    // workgroups of k_attention_spread, or 0
   size_t bytes;
 };
@@ -947,13 +991,15 @@ Plan plan_for(int total_q, int total_k, int batch, int heads_q, int heads_k, int
   // Rows by the 32 (k_attention_few): single tokens, and small grids of short
   // sequences that fit one round (256 tokens x 24 heads 9.2 -> 7.8 us; with
   // more workgroups than CUs 128-row tiles win, 512 tokens 31 against 14 us).
-  // Tiles of 128 rows: causal (4608 x 24 heads 166 -> 147 us), grids that 256
-  // rows would not fill, and few keys, where starting up is most of it (8192
+  // Tiles of 128 rows: causal (4608 x 24 heads 166 -> 147 us), grids of one
+  // such tile a CU at most, and few keys, where starting up is most of it (8192
   // rows x 10 heads over 77 and 154 keys 16 -> 13 us).  Else 256 rows, which
-  // read the keys half as often (4608 x 24 heads 270 -> 255 us).
+  // read the keys half as often (4608 x 24 heads 261 -> 246 us, 2048 x 24 62 ->
+  // 58, 1500 x 24 46 -> 42).
   const bool few = mean_rows <= 64 || (mean_rows <= 256 && units(32) <= 256);
-  p.waves = few ? 0 : causal || units(256) < 256 || mean_keys < 1024 ? 4 : 8;
+  p.waves = few ? 0 : causal || units(128) <= 256 || mean_keys < 1024 ? 4 : 8;
   p.splits = 1;
+  p.parts = 1;
   p.spread = 0;
   p.bytes = 0;
   const int64_t n = units(p.waves ? p.waves * 32 : 32);
@@ -975,11 +1021,16 @@ Plan plan_for(int total_q, int total_k, int batch, int heads_q, int heads_k, int
     p.bytes = spread_head(batch) + static_cast<size_t>(results) * 32 * (D + 2) * 4;
     return p;
   }
-  // Splits: where the tiles would leave half the CUs idle; and in two where
-  // they would give a CU one workgroup at most and the keys are long (4 heads
-  // of 128 over 4096 and 8192 keys 66 -> 54 and 190 -> 143 us, causal 66 -> 48
-  // and 127 -> 100; 8 heads over 2048 keys 37 -> 45).
-  int64_t s = n < 128 ? (256 + n - 1) / n : p.waves == 4 && n <= 256 && mean_keys >= 4096 ? 2 : 1;
+  // One tile of 128 rows a CU at most: its keys in two parts, so that each SIMD
+  // has two waves (heads of 128, tokens x heads: 1024 x 24 23.1 -> 21.6 us, 2048
+  // x 8 39 -> 32, 2048 x 16 54 -> 37, 8192 x 4 189 -> 126; with more tiles 2048
+  // x 24 62 -> 74; 600 keys no difference, 512 keys 14.0 -> 14.6).
+  if (p.waves == 4 && n <= 256 && mean_keys >= 768) p.parts = 2;
+  // Splits, where the tiles would leave half the CUs idle: until half of them
+  // have a workgroup of two parts, or all one of one (2048 x 4: 36 us whole, 30
+  // in two parts, 28 in two splits of two).
+  const int64_t enough = p.parts == 2 ? 128 : 256;
+  int64_t s = n >= 128 ? 1 : (enough + n - 1) / n;
   if (s > mean_keys / 512) s = mean_keys / 512;
   p.splits = static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
   if (p.splits > 1) p.bytes = static_cast<size_t>(p.splits) * total_q * heads_q * (D + 2) * 4;
@@ -996,14 +1047,19 @@ int launch(AttnArgs a, const Plan& p, hipStream_t stream) {
   const bool wide = a.D > 64;
   if (p.waves == 8) {
     if (wide)
-      k_attention<E, 128, 8><<<grid, 512, 0, stream>>>(a);
+      k_attention<E, 128, 8, 1><<<grid, 512, 0, stream>>>(a);
     else
-      k_attention<E, 64, 8><<<grid, 512, 0, stream>>>(a);
+      k_attention<E, 64, 8, 1><<<grid, 512, 0, stream>>>(a);
+  } else if (p.waves == 4 && p.parts == 2) {
+    if (wide)
+      k_attention<E, 128, 4, 2><<<grid, 512, 0, stream>>>(a);
+    else
+      k_attention<E, 64, 4, 2><<<grid, 512, 0, stream>>>(a);
   } else if (p.waves == 4) {
     if (wide)
-      k_attention<E, 128, 4><<<grid, 256, 0, stream>>>(a);
+      k_attention<E, 128, 4, 1><<<grid, 256, 0, stream>>>(a);
     else
-      k_attention<E, 64, 4><<<grid, 256, 0, stream>>>(a);
+      k_attention<E, 64, 4, 1><<<grid, 256, 0, stream>>>(a);
   } else if (p.spread) {
     if (wide)
       k_attention_spread<E, 128><<<p.spread, 256, 0, stream>>>(a);

@@ -160,10 +160,28 @@ def test_shares_that_end_where_a_tile_of_rows_starts(lens_q, lens_k, hq, hk, d):
 def test_long_keys_and_few_heads():
     """One workgroup a CU at most: the keys are cut in two."""
     for lens_q, lens_k, hq, hk in (([4100], [4200], 4, 4), ([2100, 4001], [8000, 300], 2, 2)):
-        assert bq.attention_workspace_size(sum(lens_q), sum(lens_k), len(lens_q), hq, hk, 40) > 0
         q, k, v = inputs(lens_q, lens_k, hq, hk, 40, BF, 9)
         for causal in (False, True):
             check(q, k, v, lens_q, lens_k, causal, "cut in two")
+
+
+@pytest.mark.parametrize("lens_q,lens_k,hq,hk,d", [
+    ([300, 20, 700, 0, 130], [1000, 0, 64, 2000, 1100], 2, 2, 128),    # parts of unequal numbers of tiles, of one and of none
+    ([500, 300], [65, 3000], 3, 3, 64),
+    ([1000], [771], 4, 1, 72),
+    ([513], [4097], 2, 2, 128),                                         # and split over workgroups as well
+])
+def test_two_parts_of_the_keys(lens_q, lens_k, hq, hk, d):
+    """A grid of few tiles of 128 rows with long keys: the waves of a
+    workgroup take them in two parts."""
+    for dtype in (BF, HF):
+        q, k, v = inputs(lens_q, lens_k, hq, hk, d, dtype, 23)
+        for causal in (False, True):
+            a, la = check(q, k, v, lens_q, lens_k, causal, "parts")
+            check(q, k, v, lens_q, lens_k, causal, "parts, whole", workspace=None)
+            args = dict(cu_seqlens_q=cu(lens_q), cu_seqlens_k=cu(lens_k), causal=causal, return_lse=True)
+            b, lb = bq.attention(q, k, v, **args)
+            assert torch.equal(a, b) and torch.equal(la, lb)
 
 
 def test_split_with_many_rows():
