@@ -29,7 +29,7 @@
 // Measured (passes over changing inputs, bf16): 4608 tokens x 24 heads of 128
 // 246 us (1060 TFLOP/s), bound by the issue of products and softmax side by
 // side and by power; one token of each of 8 caches of 0 to 16384 keys, 8 key
-// heads, 57 us (4.2 TB/s), bound by reading K and V; 77 tokens x 12 heads of
+// heads, 56 us (4.3 TB/s), bound by reading K and V; 77 tokens x 12 heads of
 // 64 in fp16, 5.2 us on the device, bound by its launch.
 
 #include <hip/hip_runtime.h>
