@@ -5,6 +5,7 @@ import ctypes
 import math
 
 import pytest
+import torch
 
 import bit_quantized_diffusion_amd as bq
 
@@ -107,3 +108,13 @@ def test_layer_norm_refuses(kw, want):
 def test_no_device_linear16_and_norm():
     assert bq.lib.svdq_linear16(*LINEAR.values(), None) == bq.SVDQ_ERR_UNSUPPORTED_DEVICE
     assert bq.lib.svdq_layer_norm(*NORM.values(), None) == bq.SVDQ_ERR_UNSUPPORTED_DEVICE
+
+
+def test_host_tensors_are_refused():
+    x, w, q = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(16, 8, dtype=torch.bfloat16), torch.zeros(4, 2, 8, dtype=torch.float16)
+    for call in (lambda: bq.linear16(x, w), lambda: bq.layer_norm(x), lambda: bq.attention(q, q, q), lambda: bq.layer_norm([1.0]),
+                 lambda: bq.linear16(x.float(), w), lambda: bq.attention(None, q, q)):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(ValueError):
+        bq.linear16(x, w, activation="relu")
