@@ -338,7 +338,7 @@ __global__ __launch_bounds__(PARTS * NW * 64, 2) void k_attention(AttnArgs a) {
   using W = WaveTile<E, DP, kKeys>;
   constexpr int kBuf = W::kBytes;
   constexpr int kLoads = kBuf / 1024 / NW;   // 1 KB loads per wave and operand tile
-  // tiles ahead of the ones in use; with 4 waves two workgroups share a CU's LDS
+  // tiles ahead of the ones in use; with 4 waves two workgroups or parts share a CU's LDS
   constexpr int kLead = NW == 8 ? 2 : 1, kSlotsK = 2 + kLead, kSlotsV = 1 + kLead;
   constexpr int kPart = (kSlotsK + kSlotsV) * kBuf;   // LDS of a part
   static_assert(kLoads >= 1 && NW * 32 * DP * 2 <= kPart, "loads divide evenly; the output staging fits");
