@@ -284,10 +284,19 @@ struct WaveTile {
       }
   }
 
-  // the two halves of a row hold the sums of different keys
-  __device__ __forceinline__ float row_sum() const {
+  // The row's sum: its two halves hold those of different keys.  A row that
+  // saw no key has no O either: a weight of zero takes a NaN or an infinity of
+  // V into it.
+  __device__ __forceinline__ float finish() {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    const float sum = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    if (sum == 0.f) {
+#pragma unroll
+      for (int d = 0; d < kDt; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[d][e] = 0.f;
+    }
+    return sum;
   }
 };
 
@@ -525,7 +534,7 @@ __global__ __launch_bounds__(PARTS * NW * 64, 2) void k_attention(AttnArgs a) {
     iterate(i, s0, s1, No{}, No{});
   }
 
-  float l = w.row_sum();
+  float l = w.finish();
   if constexpr (PARTS > 1) {
     // every part meets the barriers of the longest: two and one a tile
     static_assert(PARTS == 2, "the join is written for two");
@@ -681,7 +690,7 @@ struct Few {
     }
 
     // join the waves: common reference, then O and l scaled to it
-    const float l = w.row_sum();
+    const float l = w.finish();
     if (h == 0) lds.m[wave][l32] = w.m;
     __syncthreads();
     float m_all = lds.m[0][l32];
