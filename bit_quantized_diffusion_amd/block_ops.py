@@ -47,8 +47,9 @@ def attention(q, k, v, *, cu_seqlens_q=None, cu_seqlens_k=None, causal: bool = F
     (views into a fused QKV projection are read in place).  heads_q is a
     multiple of heads_k; query head h reads key head h // (heads_q // heads_k).
     cu_seqlens_q, cu_seqlens_k: int32 device tensors [batch+1] with the
-    sequences' starts (0 first, the total last); without them the tokens form
-    one sequence, and cu_seqlens_k defaults to cu_seqlens_q.  causal counts
+    sequences' starts (0 first, the total last; queries before the first or
+    past the last are padding, and give o = 0, lse = -inf); without them the
+    tokens form one sequence, and cu_seqlens_k defaults to cu_seqlens_q.  causal counts
     from the sequences' ends (query i sees keys j <= i + len_k - len_q).
     scale defaults to head_dim ** -0.5.  workspace: "auto" allocates what the
     schedule takes, None gives none, a uint8 tensor is used as it is.

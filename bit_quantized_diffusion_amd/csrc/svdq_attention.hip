@@ -70,6 +70,7 @@ constexpr float kSlack = 8.f;   // log2 of the largest P before a rescale
 struct Tile {
   int q0, len_q, k0, len_k;   // the sequence's tokens
   int row0, rows;             // first row of the tile, rows of the sequence
+  int held0, held1;           // find_tile: tokens of q that the sequences hold
   bool any;
 };
 
@@ -129,15 +130,37 @@ __device__ __forceinline__ Tile find_tile(const AttnArgs& a, int slot) {
     seq = max(static_cast<int>(__popcll(held)), 1) - 1;
     auto of = [](int v, int lane) { return __builtin_amdgcn_readlane(v, lane); };
     t = between(a, of(q, seq), of(q, seq + 1), of(k, seq), of(k, seq + 1));
+    t.held0 = of(q, 0), t.held1 = of(q, a.batch);
   } else {
     if (a.batch > 1) seq = last_before(a.batch, [&](int i) { return before(i, a.cu_q[i]); });
     t = sequence(a, seq);
+    t.held0 = a.cu_q ? a.cu_q[0] : 0, t.held1 = a.cu_q ? a.cu_q[a.batch] : a.total_q;
   }
+  t.held0 = min(max(t.held0, 0), a.total_q);
+  t.held1 = min(max(t.held1, t.held0), a.total_q);
   const int64_t first = static_cast<int64_t>(t.q0) * a.group / BM + seq;
   const int64_t row0 = (slot - first) * BM;
   t.any = slot >= first && row0 < t.rows;
   t.row0 = t.any ? static_cast<int>(row0) : 0;
   return t;
+}
+
+// Tokens of q that no sequence holds (before the first start, past the last)
+// see no key: o = 0, lse = -inf, by the workgroups of a key head in turn.
+template <int THREADS>
+__device__ __forceinline__ void clear_outside(const AttnArgs& a, const Tile& t, int slot, int head_k) {
+  const int outside = t.held0 + a.total_q - t.held1;
+  if (outside == 0) return;
+  const int chunks = a.D / 8, h0 = head_k * a.group;
+  for (int64_t i = slot; i < outside; i += a.slots) {
+    const int64_t token = i < t.held0 ? i : t.held1 + (i - t.held0);
+    for (int c = threadIdx.x; c < a.group * chunks; c += THREADS) {
+      const int h = c / chunks;
+      *reinterpret_cast<v4u*>(a.o + token * a.o_t + (h0 + h) * a.o_h + (c - h * chunks) * 8) = v4u{0, 0, 0, 0};
+    }
+    if (a.lse)
+      for (int h = threadIdx.x; h < a.group; h += THREADS) a.lse[token * a.heads_q + h0 + h] = -INFINITY;
+  }
 }
 
 // One K or V tile of KEYS keys in LDS: rows of DP 16-bit values, unpadded.
@@ -355,6 +378,7 @@ __global__ __launch_bounds__(PARTS * NW * 64, 2) void k_attention(AttnArgs a) {
 
   const Job job = job_of(a, blockIdx.x);
   const Tile t = find_tile<BM>(a, job.slot);
+  if (a.splits == 1) clear_outside<PARTS * NW * 64>(a, t, job.slot, job.head);   // else the join does
   if (!t.any) return;
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % NW;
@@ -739,6 +763,7 @@ __global__ __launch_bounds__(256, 1) void k_attention_few(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) typename F::Lds lds;
   const Job job = job_of(a, blockIdx.x);
   const Tile t = find_tile<F::BM>(a, job.slot);
+  clear_outside<256>(a, t, job.slot, job.head);
   if (!t.any) return;
   F::run(a, t, job.head, 0, 0x7FFFFFFF, lds);
   auto place = [&](int r, int& token, int& head) {
@@ -950,8 +975,11 @@ __global__ __launch_bounds__(256) void k_attention_join(AttnArgs a) {
   const int64_t rows = static_cast<int64_t>(a.total_q) * a.heads_q;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (row >= rows) return;
+  const int64_t tok = row / a.heads_q;
+  // no split wrote a row that no sequence holds
+  const bool held = !a.cu_q || (tok >= a.cu_q[0] && tok < a.cu_q[a.batch]);
   float2 ml = make_float2(-INFINITY, 0.f);
-  if (lane < a.splits) ml = a.part_ml[lane * rows + row];
+  if (held && lane < a.splits) ml = a.part_ml[lane * rows + row];
   float m = ml.x;
 #pragma unroll
   for (int o = 32; o; o >>= 1) {
@@ -973,7 +1001,6 @@ __global__ __launch_bounds__(256) void k_attention_join(AttnArgs a) {
       x1 += x.y * fs;
     }
   }
-  const int64_t tok = row / a.heads_q;
   if (d < a.D)
     *reinterpret_cast<uint32_t*>(a.o + tok * a.o_t + (row - tok * a.heads_q) * a.o_h + d) = E::pack2(x0 * inv, x1 * inv);
   if (a.lse && lane == 0) a.lse[row] = lse_of(m, l, a.scale);

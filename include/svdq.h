@@ -337,10 +337,12 @@ SVDQ_API int svdq_unfused_linear_noalloc(const void* x, int M, int K,
  *   lse    (dev) [total_q][heads_q] fp32, out, or NULL
  *   cu_seqlens_q, cu_seqlens_k (dev) [batch+1] int32 each: sequence b holds
  *          queries cu_q[b] .. cu_q[b+1]-1 and keys cu_k[b] .. cu_k[b+1]-1.
- *          They start at 0, do not fall and end at total_q and total_k;
- *          sequences may be empty on either side.  Values outside that are
- *          cut to [0, total], so no access leaves the tensors.  NULL (both,
- *          batch == 1): one sequence of all tokens.
+ *          They lie in [0, total] and do not fall; sequences may be empty on
+ *          either side.  Tokens of q before the first start or past the last
+ *          (padding) belong to no sequence: o = 0, lse = -inf.  With starts
+ *          that break this, o and lse are unspecified, but values outside
+ *          are cut to [0, total], so no access leaves the tensors.  NULL
+ *          (both, batch == 1): one sequence of all tokens.
  *   strides (host) 8 strides in elements: q token, q head, k token, k head,
  *          v token, v head, o token, o head.  Multiples of 8, not negative;
  *          k and v token strides in [head_dim, 2^23] when total_k > 1.  The last dimension
