@@ -2,32 +2,43 @@
 quantized linears: thin bindings over the C ABI (``include/svdq.h``), with
 torch tensors for device memory and streams.  bf16 and fp16.
 
-The arguments are checked, and the outputs allocated, by ``_block_ops.so``
-(``csrc/svdq_python.cpp``): the smallest calls take longer on the host than on
-the device.
+The arguments are checked, and the outputs allocated, by the extension
+``_block_ops`` (``csrc/svdq_python.cpp``): the smallest calls take longer on the
+host than on the device.  Without it these operators raise ImportError; the rest
+of the package needs libsvdq.so alone.
 """
 
 from __future__ import annotations
 
 import ctypes
-import os
 
 import torch
 
 from ._lib import check, lib   # loads torch's HIP runtime and libsvdq.so first
 
-if not os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_block_ops.so")):
-    raise ImportError("_block_ops.so is missing: build it with `python bit_quantized_diffusion_amd/build.py`")
 
-from . import _block_ops   # noqa: E402
+class _Missing:
+    """In the place of an extension that is not there for this Python."""
 
-# the current stream's handle without a Stream object around it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda device: torch.cuda.current_stream(device).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    def __init__(self, why: ImportError):
+        self._why = why
 
-_block_ops.setup(torch.Tensor, torch.bfloat16, torch.float16, torch.float32, torch.uint8, torch.int32, _raw_stream,
-                 _current_device, torch.cuda.set_device, check)
+    def __getattr__(self, name):
+        raise ImportError(f"{name} needs the extension _block_ops, built for this Python by "
+                          f"`python bit_quantized_diffusion_amd/build.py`: {self._why}") from self._why
+
+
+try:
+    from . import _block_ops
+except ImportError as e:
+    _block_ops = _Missing(e)
+else:
+    # the current stream's handle without a Stream object around it
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _block_ops.setup(torch.Tensor, torch.bfloat16, torch.float16, torch.float32, torch.uint8, torch.int32, _raw_stream,
+                     _current_device, torch.cuda.set_device, check)
 
 
 def attention_workspace_size(total_q: int, total_k: int, batch: int, heads_q: int, heads_k: int, head_dim: int) -> int:

@@ -1,5 +1,6 @@
-"""Build libsvdq.so in-tree with hipcc for gfx950, and _block_ops.so, the
-Python side of the 16-bit block operators.
+"""Build libsvdq.so in-tree with hipcc for gfx950, and then _block_ops, the
+Python side of the 16-bit block operators.  libsvdq.so serves any Python;
+_block_ops needs Python's headers and is named for the Python it is built for.
 
     python bit_quantized_diffusion_amd/build.py [-v]
 
@@ -25,7 +26,7 @@ import tempfile
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsvdq.so")
-PYTHON_LIB = os.path.join(PKG, "_block_ops.so")
+PYTHON_LIB = os.path.join(PKG, "_block_ops" + sysconfig.get_config_var("EXT_SUFFIX"))
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")
 CLANGXX = os.path.join(ROCM, "llvm", "bin", "clang++")
@@ -59,9 +60,15 @@ def _run(cmd, verbose):
         sys.stderr.write(rest + "\n")
 
 
+def _install(built, path):
+    staged = path + ".tmp"
+    shutil.copyfile(built, staged)
+    os.replace(staged, path)
+
+
 def build(verbose: bool = False) -> str:
     """Compile every source and link both libraries; returns the path of
-    libsvdq.so."""
+    libsvdq.so, which is installed also where _block_ops fails to build."""
     tmp = tempfile.mkdtemp(prefix="svdq_build_")
     try:
         objs = []
@@ -73,9 +80,6 @@ def build(verbose: bool = False) -> str:
         for src in HOST_SOURCES:
             obj = os.path.join(tmp, src + ".o")
             procs.append(([compiler, "-x", "c++", *HOST_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj], obj))
-        python_obj = os.path.join(tmp, PYTHON_SOURCE + ".o")
-        procs.append(([compiler, "-x", "c++", *HOST_FLAGS, f"-I{sysconfig.get_paths()['include']}", "-c",
-                       os.path.join(CSRC, PYTHON_SOURCE), "-o", python_obj], python_obj))
         running = [(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True), cmd, obj)
                    for cmd, obj in procs]
         for p, cmd, obj in running:
@@ -85,18 +89,17 @@ def build(verbose: bool = False) -> str:
                 raise RuntimeError(f"build step failed: {' '.join(cmd)}")
             if verbose:
                 print(" ".join(cmd), flush=True)
-            if obj != python_obj:
-                objs.append(obj)
+            objs.append(obj)
         tmp_lib = os.path.join(tmp, "libsvdq.so")
         _run([HIPCC, "-shared", f"--offload-arch={ARCH}", "-fPIC", "-pthread", "-o", tmp_lib, *objs], verbose)
+        _install(tmp_lib, LIB)
         # finds libsvdq.so beside itself
-        tmp_python = os.path.join(tmp, "_block_ops.so")
+        python_obj, tmp_python = os.path.join(tmp, PYTHON_SOURCE + ".o"), os.path.join(tmp, "_block_ops.so")
+        _run([compiler, "-x", "c++", *HOST_FLAGS, f"-I{sysconfig.get_paths()['include']}", "-c",
+              os.path.join(CSRC, PYTHON_SOURCE), "-o", python_obj], verbose)
         _run([compiler, "-shared", "-o", tmp_python, python_obj, f"-L{tmp}", "-l:libsvdq.so", "-Wl,-rpath,$ORIGIN"],
              verbose)
-        for built, path in ((tmp_lib, LIB), (tmp_python, PYTHON_LIB)):
-            staged = path + ".tmp"
-            shutil.copyfile(built, staged)
-            os.replace(staged, path)
+        _install(tmp_python, PYTHON_LIB)
         return LIB
     finally:
         shutil.rmtree(tmp, ignore_errors=True)
