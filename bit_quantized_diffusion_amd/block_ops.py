@@ -76,8 +76,8 @@ ACTIVATIONS = {"none": 0, "gelu": 1, "silu": 2}
 
 
 def linear16_workspace_size(M: int, N: int, K: int) -> int:
-    """Bytes of workspace with which `linear16` cuts small grids along K (0:
-    it runs them in one piece anyway)."""
+    """Bytes of workspace with which `linear16` cuts small grids along K,
+    whatever its operands' alignment (0: it runs them in one piece anyway)."""
     out = ctypes.c_size_t(0)
     check(lib.svdq_linear16_workspace_size(M, N, K, ctypes.byref(out)))
     return int(out.value)

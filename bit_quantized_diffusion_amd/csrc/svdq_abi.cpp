@@ -360,7 +360,21 @@ int svdq_linear16_workspace_size(int M, int N, int K, size_t* out_bytes) {
   *out_bytes = 0;
   const int st = check_linear16_shape(M, N, K);
   if (st) return st;
-  *out_bytes = svdq_linear16_plan_bytes(M, N, K);
+  *out_bytes = svdq_linear16_plan_bytes(M, N, K, 0);
+  if (K % 8 == 0) {
+    const size_t aligned = svdq_linear16_plan_bytes(M, N, K, 1);
+    if (aligned > *out_bytes) *out_bytes = aligned;
+  }
+  return SVDQ_OK;
+}
+
+int svdq_linear16_workspace_size_for(const void* x, int64_t ldx, const void* w, int64_t ldw, int M, int N, int K,
+                                     size_t* out_bytes) {
+  if (!out_bytes) return SVDQ_ERR_INVALID_ARG;
+  *out_bytes = 0;
+  const int st = check_linear16_shape(M, N, K);
+  if (st) return st;
+  *out_bytes = svdq_linear16_plan_bytes(M, N, K, svdq_linear16_aligned(x, ldx, w, ldw, K));
   return SVDQ_OK;
 }
 

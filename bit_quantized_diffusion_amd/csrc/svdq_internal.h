@@ -85,8 +85,10 @@ int svdq_launch_attention(const void* q, const void* k, const void* v, void* o, 
                           const int32_t* cu_k, int batch, int total_q, int total_k, int heads_q, int heads_k,
                           int head_dim, const int64_t* strides, float scale, int causal, int dtype, void* workspace,
                           size_t workspace_bytes, void* stream);
-// Workspace bytes of svdq_launch_linear16 for these sizes (0: no split).
-size_t svdq_linear16_plan_bytes(int M, int N, int K);
+// Whether svdq_launch_linear16 takes these rows with 16-byte loads, and its
+// workspace bytes for these sizes (0: no split).
+int svdq_linear16_aligned(const void* x, int64_t ldx, const void* w, int64_t ldw, int K);
+size_t svdq_linear16_plan_bytes(int M, int N, int K, int aligned);
 int svdq_launch_linear16(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const void* gate,
                          int64_t ld_gate, int group_rows, const void* residual, int64_t ldr, void* y, int64_t ldy, int M,
                          int N, int K, int activation, int dtype, void* workspace, size_t workspace_bytes, void* stream);

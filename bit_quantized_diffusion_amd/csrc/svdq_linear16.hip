@@ -603,18 +603,17 @@ struct Plan {
 // reads and writes them once more, and its launch and workspace cost the host
 // as much again as the call (128 x 512 x 2048 whole 9.0 us, split 11.7; 128 x
 // 512 x 4096 16.1 and 12.4; 238 x 235 x 7556 54 and 23).
-Plan plan_for(int M, int N, int K, bool aligned, size_t most) {
+Plan plan_for(int M, int N, int K, bool aligned, int most_splits) {
   const int stages = (K + 63) / 64;
   Plan best{kAny64, 1, stages, 0};
   float least = INFINITY;
   for (int i = aligned ? 0 : kAny128; i < (aligned ? kAny128 : kShapes); ++i) {
     const Shape& c = kShape[i];
     const float tiles = static_cast<float>((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
-    for (int s = 1; s <= kMaxSplits && s <= stages; ++s) {
+    for (int s = 1; s <= most_splits && s <= stages; ++s) {
       const int per = (stages + s - 1) / s;
       if ((stages + per - 1) / per != s) continue;
       const size_t bytes = s == 1 ? 0 : static_cast<size_t>(s) * M * N * 4;
-      if (bytes > most) break;
       const float groups = tiles * s, load = groups / c.slots;
       const float stage = c.light + (c.full - c.light) * fminf(fmaxf(groups - 256.f * (c.slots > 256), 0.f) / 256.f, 1.f);
       const float rounds = load <= 1.f ? 1.f : 0.5f * (load + ceilf(load));
@@ -660,7 +659,9 @@ int launch(LinArgs a, bool aligned, size_t workspace, hipStream_t stream) {
       k_linear16_few<E, 8, 4><<<blocks, 256, 0, stream>>>(a);
     return static_cast<int>(hipGetLastError());
   }
-  const Plan p = plan_for(a.M, a.N, a.K, aligned, workspace);
+  // the sum's order goes by the sizes: all of the workspace, or one piece
+  Plan p = plan_for(a.M, a.N, a.K, aligned, kMaxSplits);
+  if (workspace < p.bytes) p = plan_for(a.M, a.N, a.K, aligned, 1);
   a.splits = p.splits;
   a.stages_per_split = p.per;
   switch (p.shape) {
@@ -682,9 +683,13 @@ int launch(LinArgs a, bool aligned, size_t workspace, hipStream_t stream) {
 
 extern "C" {
 
-size_t svdq_linear16_plan_bytes(int M, int N, int K) {
-  const bool aligned = K % 8 == 0;
-  return aligned && M <= kFewRows ? 0 : plan_for(M, N, K, aligned, SIZE_MAX).bytes;
+int svdq_linear16_aligned(const void* x, int64_t ldx, const void* w, int64_t ldw, int K) {
+  return K % 8 == 0 && ldx % 8 == 0 && ldw % 8 == 0 &&
+         ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 15) == 0;
+}
+
+size_t svdq_linear16_plan_bytes(int M, int N, int K, int aligned) {
+  return aligned && M <= kFewRows ? 0 : plan_for(M, N, K, aligned, kMaxSplits).bytes;
 }
 
 int svdq_launch_linear16(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const void* gate,
@@ -709,8 +714,7 @@ int svdq_launch_linear16(const void* x, int64_t ldx, const void* w, int64_t ldw,
   a.group_rows = group_rows;
   a.act = activation;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool aligned = K % 8 == 0 && ldx % 8 == 0 && ldw % 8 == 0 &&
-                       ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 15) == 0;
+  const bool aligned = svdq_linear16_aligned(x, ldx, w, ldw, K);
   const size_t bytes = workspace ? workspace_bytes : 0;
   return dtype == SVDQ_BF16 ? launch<Bf16>(a, aligned, bytes, s) : launch<F16>(a, aligned, bytes, s);
 }

@@ -443,7 +443,7 @@ PyObject* linear16(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (M == 0) return out.release();
   const int m = static_cast<int>(M), nn = static_cast<int>(N), k = static_cast<int>(K);
   size_t bytes = 0, size;
-  if (args[8] != Py_None && !fine(svdq_linear16_workspace_size(m, nn, k, &bytes))) return nullptr;
+  if (args[8] != Py_None && !fine(svdq_linear16_workspace_size_for(x.ptr, x.ld(), w.ptr, w.ld(), m, nn, k, &bytes))) return nullptr;
   void* ws;
   Ref keep;
   if (!workspace_of(args[8], args[0], x, bytes, ws, size, keep)) return nullptr;

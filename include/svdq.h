@@ -394,14 +394,18 @@ SVDQ_API int svdq_attention(const void* q, const void* k, const void* v, void* o
  * alignment only; rows of x and w that are 16-byte aligned with
  * K % 8 == 0 take the faster loads.
  * workspace (dev, 16-byte aligned): with the bytes that
- * svdq_linear16_workspace_size names, grids that would leave the device
- * idle are cut along K into fp32 parts that a second kernel adds in a fixed
- * order; with NULL or fewer bytes they run in one piece.  Results are
- * deterministic. */
+ * svdq_linear16_workspace_size names (at any alignment), or those that
+ * svdq_linear16_workspace_size_for names for these operands (their addresses
+ * and strides alone are looked at), grids that would leave the device idle
+ * are cut along K into fp32 parts that a second kernel adds in a fixed
+ * order; with NULL or fewer bytes than the latter they run in one piece.
+ * Results are deterministic. */
 #define SVDQ_ACT_NONE  0
 #define SVDQ_ACT_GELU  1
 #define SVDQ_ACT_SILU  2
 SVDQ_API int svdq_linear16_workspace_size(int M, int N, int K, size_t* out_bytes);
+SVDQ_API int svdq_linear16_workspace_size_for(const void* x, int64_t ldx, const void* w, int64_t ldw,
+                              int M, int N, int K, size_t* out_bytes);
 SVDQ_API int svdq_linear16(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
                               const void* gate, int64_t ld_gate, int group_rows,
                               const void* residual, int64_t ldr, void* y, int64_t ldy,

@@ -118,3 +118,24 @@ def test_host_tensors_are_refused():
             call()
     with pytest.raises(ValueError):
         bq.linear16(x, w, activation="relu")
+
+
+def test_linear16_workspace_size_for_operands():
+    """The plan goes by the operands' alignment; the query without them names
+    enough for either."""
+    f = bq.lib.svdq_linear16_workspace_size_for
+    out = ctypes.c_size_t(7)
+
+    def named(x, ldx, w, ldw, m, n, k):
+        assert f(x, ldx, w, ldw, m, n, k, ctypes.byref(out)) == 0
+        return out.value
+
+    assert f(FAKE, 64, FAKE, 64, 1, 1, 64, None) == BAD
+    assert f(FAKE, 64, FAKE, 64, 0, 1, 64, ctypes.byref(out)) == SHAPE and out.value == 0
+    for m, n, k in ((16, 64, 15360), (1, 32, 8192), (32, 512, 4096)):   # up to 32 rows: only misaligned ones are split
+        assert named(FAKE, k, FAKE, k, m, n, k) == 0
+        for args in ((ODD, k, FAKE, k), (FAKE, k, ODD, k), (FAKE, k + 1, FAKE, k), (FAKE, k, FAKE, k + 4)):
+            assert 0 < named(*args, m, n, k) <= bq.linear16_workspace_size(m, n, k)
+    for m, n, k in ((100, 256, 4096), (40, 130, 2056), (333, 512, 8192), (300, 33, 1024), (4608, 128, 15360)):
+        most = max(named(FAKE, k, FAKE, k, m, n, k), named(ODD, k, FAKE, k, m, n, k))
+        assert bq.linear16_workspace_size(m, n, k) == most
