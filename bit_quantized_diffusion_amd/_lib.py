@@ -34,6 +34,7 @@ EXPORTED = (
     "svdq_unfused_linear_noalloc", "svdq_gemm_workspace_size", "svdq_gemm_w4a4_lora_up_ws",
     "svdq_attention_workspace_size", "svdq_attention",
     "svdq_linear16_workspace_size", "svdq_linear16_workspace_size_for", "svdq_linear16", "svdq_layer_norm",
+    "svdq_debug_attention_plan", "svdq_debug_linear16_plan",
 )
 
 
@@ -80,6 +81,8 @@ def _load():
         "svdq_linear16_workspace_size": ([i, i, i, sz], i),
         "svdq_linear16_workspace_size_for": ([vp, l, vp, l, i, i, i, sz], i),
         "svdq_linear16": ([vp, l, vp, l, vp, vp, l, i, vp, l, vp, l, i, i, i, i, i, vp, ctypes.c_size_t, vp], i),
+        "svdq_debug_attention_plan": ([i, i, i, i, i, i, i, vp], i),
+        "svdq_debug_linear16_plan": ([i, i, i, i, vp], i),
         "svdq_layer_norm": ([vp, l, vp, vp, vp, vp, l, i, vp, l, i, i, ctypes.c_float, i, vp], i),
         "svdq_attention_workspace_size": ([i, i, i, i, i, i, sz], i),
         "svdq_attention": ([vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp, ctypes.c_float, i, i, vp, ctypes.c_size_t,

@@ -439,4 +439,22 @@ int svdq_debug_group_partials(const uint8_t* xq, const uint8_t* wq, int M, int N
   return hip_status(svdq_launch_debug_group_partials(xq, wq, M, N, K, m0, n0, mt, nt, out, stream));
 }
 
+int svdq_debug_attention_plan(int total_q, int total_k, int batch, int heads_q, int heads_k, int head_dim, int causal,
+                              int32_t* plan) {
+  if (!plan) return SVDQ_ERR_INVALID_ARG;
+  const int st = check_attention_shape(total_q, total_k, batch, heads_q, heads_k, head_dim);
+  if (st) return st;
+  svdq_attention_plan(total_q, total_k, batch, heads_q, heads_k, head_dim, causal, plan);
+  return SVDQ_OK;
+}
+
+int svdq_debug_linear16_plan(int M, int N, int K, int aligned, int32_t* plan) {
+  if (!plan) return SVDQ_ERR_INVALID_ARG;
+  const int st = check_linear16_shape(M, N, K);
+  if (st) return st;
+  if (aligned && K % 8) return SVDQ_ERR_SHAPE;
+  svdq_linear16_plan(M, N, K, aligned, plan);
+  return SVDQ_OK;
+}
+
 }  // extern "C"

@@ -1125,6 +1125,14 @@ size_t svdq_attention_plan_bytes(int total_q, int total_k, int batch, int heads_
   return full > causal ? full : causal;
 }
 
+void svdq_attention_plan(int total_q, int total_k, int batch, int heads_q, int heads_k, int head_dim, int causal, int32_t* plan) {
+  const Plan p = plan_for(total_q, total_k, batch, heads_q, heads_k, head_dim, causal);
+  plan[0] = p.waves ? p.waves * 32 : 32;
+  plan[1] = p.parts;
+  plan[2] = p.splits;
+  plan[3] = p.spread;
+}
+
 int svdq_launch_attention(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_q,
                           const int32_t* cu_k, int batch, int total_q, int total_k, int heads_q, int heads_k,
                           int head_dim, const int64_t* strides, float scale, int causal, int dtype, void* workspace,

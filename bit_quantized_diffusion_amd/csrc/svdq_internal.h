@@ -89,6 +89,9 @@ int svdq_launch_attention(const void* q, const void* k, const void* v, void* o, 
 // workspace bytes for these sizes (0: no split).
 int svdq_linear16_aligned(const void* x, int64_t ldx, const void* w, int64_t ldw, int K);
 size_t svdq_linear16_plan_bytes(int M, int N, int K, int aligned);
+// The schedules, as svdq.h's test hooks give them.
+void svdq_attention_plan(int total_q, int total_k, int batch, int heads_q, int heads_k, int head_dim, int causal, int32_t* plan);
+void svdq_linear16_plan(int M, int N, int K, int aligned, int32_t* plan);
 int svdq_launch_linear16(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const void* gate,
                          int64_t ld_gate, int group_rows, const void* residual, int64_t ldr, void* y, int64_t ldy, int M,
                          int N, int K, int activation, int dtype, void* workspace, size_t workspace_bytes, void* stream);

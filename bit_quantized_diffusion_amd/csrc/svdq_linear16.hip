@@ -578,17 +578,17 @@ __global__ __launch_bounds__(NW * 64, 1) void k_linear16_few(LinArgs a) {
 // and with every slot taken; `fixed`: launch, first loads and epilogue.
 // Measured on bf16 normal values with K from 512 to 12288.
 struct Shape {
-  int bn, bm, slots;
+  int bn, bm, waves, slots;
   float light, full, fixed;
 };
 enum { k256, k128, k128Deep, k64, kAny128, kAny64, kShapes };
 constexpr Shape kShape[kShapes] = {
-    {256, 256, 256, 1.10f, 1.45f, 8.f},   // 8 waves
-    {128, 128, 512, 0.50f, 0.83f, 5.f},   // 4 waves, two workgroups a CU
-    {128, 128, 256, 0.36f, 0.42f, 5.f},   // 8 waves, loads two stages further ahead
-    {64, 64, 512, 0.20f, 0.33f, 4.f},     // 4 waves, one stage further ahead
-    {128, 128, 512, 1.00f, 1.60f, 5.f},   // k_linear16_any, two stages ahead
-    {64, 64, 512, 0.38f, 0.65f, 4.f},     // k_linear16_any, three stages ahead
+    {256, 256, 8, 256, 1.10f, 1.45f, 8.f},
+    {128, 128, 4, 512, 0.50f, 0.83f, 5.f},   // two workgroups a CU
+    {128, 128, 8, 256, 0.36f, 0.42f, 5.f},   // loads two stages further ahead
+    {64, 64, 4, 512, 0.20f, 0.33f, 4.f},     // one stage further ahead
+    {128, 128, 4, 512, 1.00f, 1.60f, 5.f},   // k_linear16_any, two stages ahead
+    {64, 64, 4, 512, 0.38f, 0.65f, 4.f},     // k_linear16_any, three stages ahead
 };
 constexpr int kMaxSplits = 8;
 
@@ -629,6 +629,8 @@ Plan plan_for(int M, int N, int K, bool aligned, int most_splits) {
 
 // up to 32 rows the weights are read once by k_linear16_few
 constexpr int kFewRows = 32;
+// waves of its workgroups: two from 9 rows on where there are more of them than CUs
+int few_waves(int M, int N) { return M > 8 && (N + 31) / 32 > 256 ? 2 : 4; }
 
 dim3 tiles(const LinArgs& a, int bn, int bm) {
   return dim3(static_cast<unsigned>((a.M + bm - 1) / bm) * static_cast<unsigned>((a.N + bn - 1) / bn), a.splits);
@@ -644,16 +646,16 @@ int launch(LinArgs a, bool aligned, size_t workspace, hipStream_t stream) {
   a.splits = 1;
   if (aligned && a.M <= kFewRows) {
     const unsigned blocks = (a.N + 31) / 32;
-    const bool many = blocks > 256;
+    const bool two = few_waves(a.M, a.N) == 2;
     if (a.M <= 4)
       k_linear16_few<E, 1, 4><<<blocks, 256, 0, stream>>>(a);
     else if (a.M <= 8)
       k_linear16_few<E, 2, 4><<<blocks, 256, 0, stream>>>(a);
-    else if (a.M <= 16 && many)
+    else if (a.M <= 16 && two)
       k_linear16_few<E, 4, 2><<<blocks, 128, 0, stream>>>(a);
     else if (a.M <= 16)
       k_linear16_few<E, 4, 4><<<blocks, 256, 0, stream>>>(a);
-    else if (many)
+    else if (two)
       k_linear16_few<E, 8, 2><<<blocks, 128, 0, stream>>>(a);
     else
       k_linear16_few<E, 8, 4><<<blocks, 256, 0, stream>>>(a);
@@ -690,6 +692,20 @@ int svdq_linear16_aligned(const void* x, int64_t ldx, const void* w, int64_t ldw
 
 size_t svdq_linear16_plan_bytes(int M, int N, int K, int aligned) {
   return aligned && M <= kFewRows ? 0 : plan_for(M, N, K, aligned, kMaxSplits).bytes;
+}
+
+void svdq_linear16_plan(int M, int N, int K, int aligned, int32_t* plan) {
+  if (aligned && M <= kFewRows) {
+    plan[0] = plan[1] = 32;
+    plan[2] = few_waves(M, N);
+    plan[3] = 1;
+    return;
+  }
+  const Plan p = plan_for(M, N, K, aligned, kMaxSplits);
+  plan[0] = kShape[p.shape].bm;
+  plan[1] = kShape[p.shape].bn;
+  plan[2] = kShape[p.shape].waves;
+  plan[3] = p.splits;
 }
 
 int svdq_launch_linear16(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, const void* gate,

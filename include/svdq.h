@@ -455,6 +455,18 @@ SVDQ_API int svdq_debug_group_partials(const uint8_t* xq, const uint8_t* wq,
                               int m0, int n0, int mt, int nt,
                               int32_t* out, void* stream);
 
+/* Test hooks (host): the schedule that svdq_attention and svdq_linear16 take
+ * for these sizes, given the workspace that they name for them.
+ *   attention: plan[0] rows of a tile, [1] parts of its keys within a
+ *   workgroup, [2] splits of them over workgroups, [3] workgroups that take
+ *   equal shares of all keys (0: a tile's keys are one workgroup's)
+ *   linear16: plan[0] rows and [1] channels of a tile, [2] waves of a
+ *   workgroup, [3] splits along K; aligned != 0: rows of x and w are 16-byte
+ *   aligned, which takes K % 8 == 0 */
+SVDQ_API int svdq_debug_attention_plan(int total_q, int total_k, int batch, int heads_q,
+                              int heads_k, int head_dim, int causal, int32_t* plan);
+SVDQ_API int svdq_debug_linear16_plan(int M, int N, int K, int aligned, int32_t* plan);
+
 #ifdef __cplusplus
 }
 #endif

@@ -59,13 +59,17 @@ def test_rows_without_keys_are_zero_beside_values_that_are_not_finite(lens_q, le
 # (lens_q, lens_k, heads_q, heads_k, head_dim, causal), one for each schedule
 SCHEDULES = [
     ([20, 0, 31], [40, 9, 100], 4, 2, 128, True),         # tiles of 32 rows, one workgroup through all keys
-    ([1, 2, 1], [900, 0, 3000], 4, 2, 64, False),         # the same with equal shares of the keys over workgroups
+    ([300, 200], [200, 90], 3, 3, 64, True),
     ([1] * 70, [0, 5, 64] * 23 + [3000], 2, 1, 40, True),   # more sequences than the lanes of a wave hold
-    ([300, 200], [200, 90], 3, 3, 64, True),              # tiles of 128 rows
+    ([1, 2, 1], [900, 0, 3000], 4, 2, 64, False),         # the same with equal shares of the keys over workgroups
+    ([600, 500], [700, 400], 3, 3, 64, True),             # tiles of 128 rows
     ([1000], [900], 2, 2, 128, False),                    # the keys in two parts within a workgroup
     ([700, 500], [2000, 2100], 2, 1, 72, False),          # and split over workgroups
     ([1100, 0, 1301], [1900, 40, 1300], 16, 8, 64, False),    # tiles of 256 rows
 ]
+# (rows of a tile, parts, whether split, whether equal shares) of each
+PLANS = [(32, 1, False, False)] * 3 + [(32, 1, False, True), (128, 1, False, False), (128, 2, False, False),
+                                       (128, 2, True, False), (256, 1, False, False)]
 
 
 def packed(lens_q, lens_k, hq, hk, d, dtype, front, back):
