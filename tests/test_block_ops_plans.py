@@ -3,10 +3,13 @@ refuse, and that the GPU tests' sizes reach every kernel."""
 
 import ctypes
 
+import pytest
+
 import bit_quantized_diffusion_amd as bq
 from tests import test_gpu_attention_rows as rows
 from tests import test_gpu_attention_wide as wide
-from tests._plans import attention_plan
+from tests import test_gpu_linear16_tiles as tiles
+from tests._plans import attention_plan, linear16_plan
 
 BAD, SHAPE = bq.SVDQ_ERR_INVALID_ARG, bq.SVDQ_ERR_SHAPE
 
@@ -26,3 +29,15 @@ def test_attention_sizes_reach_every_schedule():
         assert (height, parts, splits > 1, shares > 0) == want, case
     for case in wide.CASES:
         assert attention_plan(*case, False) == (256, 1, 1, 0), case
+
+
+def test_linear16_sizes_reach_every_tile_shape():
+    for case, want in tiles.TILES.items():
+        assert linear16_plan(*case) == want, case
+    shapes = {(c[3], *p[:3], p[3] > 1) for c, p in tiles.TILES.items()}
+    assert len(shapes) >= 11
+
+
+@pytest.mark.parametrize("m,n,waves", [(1, 64, 4), (8, 20000, 4), (9, 8192, 4), (9, 8193, 2), (32, 20000, 2)])
+def test_few_rows(m, n, waves):
+    assert linear16_plan(m, n, 512, True) == (32, 32, waves, 1)
