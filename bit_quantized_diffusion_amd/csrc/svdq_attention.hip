@@ -328,7 +328,9 @@ __device__ __forceinline__ float lse_of(float m, float l, float scale) { return 
 // Workgroup -> (slot, key head, split).  The workgroups of one (head, split)
 // read the same keys; where the units divide evenly, each of the 8 XCDs
 // (consecutive ids go to consecutive XCDs) takes whole units, so that its L2
-// holds them.  Causal tiles run longest first.
+// holds them.  Causal tiles run from the last to the first: a sequence's
+// longest first, the sequences of a pack in reverse order whatever their
+// lengths.
 struct Job {
   int slot, head, split;
 };
@@ -1040,18 +1042,22 @@ Plan plan_for(int total_q, int total_k, int batch, int heads_q, int heads_k, int
   p.bytes = 0;
   const int64_t n = units(p.waves ? p.waves * 32 : 32);
   if (p.waves == 0) {
-    // Where the tiles of rows would not give every CU two workgroups and the
-    // keys are long, one workgroup a CU with equal shares of at least 12 units.
+    // Where the tiles of rows are fewer than the CUs and the keys are long,
+    // one workgroup a CU with equal shares of at least 12 units.
     // One token over so many keys, in one workgroup a head and spread, the
     // second kernel with it (24 heads of 128): 300 keys 8 and 14 us, 1000 keys
     // 15 and 15, 2000 keys 24 and 16, 4000 keys 54 and 22.  Of several
     // sequences the mean alone is known but the longest counts: from 256 keys
-    // (4 of 300 each 8 and 14 us, 5 of 1342 .. 1 18 and 17).
+    // (4 of 300 each 8 and 14 us, 5 of 1342 .. 1 18 and 17).  From as many tiles
+    // of rows as CUs on each keeps its workgroup: with equal caches that is
+    // faster (64 of 2000 keys, 8 key heads of 128: 96 and 108 us in equal
+    // shares, of 64: 53 and 61), with one long cache among short ones much
+    // slower (16384 with 63 of 100: 183 and 34, 112 and 24).
     const int64_t tiles = (mean_keys + 31) / 32;
     if (tiles <= (batch == 1 ? 32 : 8)) return p;
     int64_t w = n / heads_k * (tiles + kStartUnits) * heads_k / 12;
     if (w > 256) w = 256;
-    if (n >= 512 || batch > kSpreadBatch || w <= n) return p;
+    if (batch > kSpreadBatch || w <= n) return p;
     p.spread = static_cast<int>(w);
     const int64_t results = w + (rows / 32 + batch) * heads_k;
     p.bytes = spread_head(batch) + static_cast<size_t>(results) * 32 * (D + 2) * 4;

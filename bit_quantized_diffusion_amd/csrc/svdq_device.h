@@ -62,11 +62,6 @@ struct F16 {
   }
 };
 
-template <typename E>
-__device__ __forceinline__ float to_f32(uint16_t b) { return E::lo(b); }
-template <typename E>
-__device__ __forceinline__ uint16_t from_f32(float f) { return static_cast<uint16_t>(E::pack2(f, 0.f)); }
-
 // Buffer descriptor of `bytes` bytes at base (at most 2^31 - 1): loads past
 // the end return zeros, also those that go to LDS.  kOutside is an offset
 // that lies past the end of every such buffer.
@@ -131,13 +126,6 @@ __device__ __forceinline__ v4u lds_read16(uint32_t a) {
 __device__ __forceinline__ v2u lds_read_tr(uint32_t a) {
   return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                      reinterpret_cast<__attribute__((address_space(3))) v4s*>(a)));
-}
-
-// the value the lane 32 lanes away holds
-__device__ __forceinline__ float other_half(float v) {
-  const uint32_t u = __float_as_uint(v);
-  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
 }
 
 // 8 elements at any 2-byte aligned address (global memory takes unaligned

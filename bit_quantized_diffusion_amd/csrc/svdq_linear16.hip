@@ -108,7 +108,7 @@ template <typename E, int BN, int BM, int WN, int WM, int TN, int TM, int JP>
 __device__ __forceinline__ void epilogue(const LinArgs& a, const v4f (&acc)[TN][TM], uint8_t* lds, int m0, int n0) {
   constexpr int kThreads = WN * WM * 64, kC4 = BN / 4, kLanesRow = BN / 8, kPass = kThreads / kLanesRow;
   constexpr int kRowsJ = JP * WM * 16, kIter = kRowsJ / kPass;
-  static_assert(kC4 % 16 == 0 && TM % JP == 0 && kThreads % kLanesRow == 0 && kRowsJ % kPass == 0 && true,
+  static_assert(kC4 % 16 == 0 && TM % JP == 0 && kThreads % kLanesRow == 0 && kRowsJ % kPass == 0,
                 "the swizzle stays inside a row; whole passes");
   float* const stage = reinterpret_cast<float*>(lds);
   const int l16 = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3, wave = threadIdx.x >> 6;
