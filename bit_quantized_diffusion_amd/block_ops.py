@@ -6,6 +6,9 @@ The arguments are checked, and the outputs allocated, by the extension
 ``_block_ops`` (``csrc/svdq_python.cpp``): the smallest calls take longer on the
 host than on the device.  Without it these operators raise ImportError; the rest
 of the package needs libsvdq.so alone.
+
+Forward only: results carry no gradient, also where an operand requires one (the
+quantized layers around them have none).
 """
 
 from __future__ import annotations
@@ -62,13 +65,13 @@ def attention(q, k, v, *, cu_seqlens_q=None, cu_seqlens_k=None, causal: bool = F
     past the last are padding, and give o = 0, lse = -inf); without them the
     tokens form one sequence, and cu_seqlens_k defaults to cu_seqlens_q.  causal counts
     from the sequences' ends (query i sees keys j <= i + len_k - len_q).
-    scale defaults to head_dim ** -0.5.  workspace: "auto" allocates what the
+    scale defaults to head_dim ** -0.5.  A NaN or infinity in v at a key that
+    causal alone hides from a query can reach it.  workspace: "auto" allocates what the
     schedule takes, None gives none, a uint8 tensor is used as it is.
 
     Returns o (like q, contiguous unless `out` is given, which overlaps none
-    of q, k and v) or, with
-    return_lse, (o, lse fp32 [total_q][heads_q]).  A query that sees no key
-    gives o = 0, lse = -inf."""
+    of q, k and v) or, with return_lse, (o, lse fp32 [total_q][heads_q]).  A
+    query that sees no key gives o = 0, lse = -inf.  No gradient."""
     return _block_ops.attention(q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale, out, return_lse, workspace)
 
 
@@ -92,7 +95,7 @@ def linear16(x, w, bias=None, *, activation: str = "none", gate=None, residual=N
     [N], or [groups][N] with row r taking group r // group_rows (group_rows
     defaults to M / groups).  activation: "none", "gelu" (tanh form) or
     "silu".  Rows may be strided.  `out` may be `residual`.  workspace: as
-    for `attention`."""
+    for `attention`.  No gradient."""
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation: expected one of {tuple(ACTIVATIONS)}, got {activation!r}")
@@ -106,5 +109,5 @@ def layer_norm(x, weight=None, bias=None, *, scale=None, shift=None, group_rows=
 
     weight, bias [K]; scale, shift [K], or [groups][K] with row r taking group
     r // group_rows (group_rows defaults to M / groups).  Rows may be
-    strided.  `out` may be x."""
+    strided.  `out` may be x.  No gradient."""
     return _block_ops.layer_norm(x, weight, bias, scale, shift, group_rows, eps, out)
