@@ -27,10 +27,11 @@
 // even for the matrix core and l sums the unrounded values.
 //
 // Measured (passes over changing inputs, bf16): 4608 tokens x 24 heads of 128
-// 246 us (1060 TFLOP/s), bound by the issue of products and softmax side by
-// side and by power; one token of each of 8 caches of 0 to 16384 keys, 8 key
-// heads, 56 us (4.3 TB/s), bound by reading K and V; 77 tokens x 12 heads of
-// 64 in fp16, 5.2 us on the device, bound by its launch.
+// 247 to 255 us over boxes (1060 to 1020 TFLOP/s), bound by power (the same
+// loop on zeros runs at 1470); one token of each of 8 caches of 0 to 16384
+// keys, 8 key heads, 56 us (4.3 TB/s), bound by reading K and V; 77 tokens x
+// 12 heads of 64 in fp16, 5.2 us on the device, bound by its launch.  P in 16
+// bits makes the error against 64 bits up to 1.41 times that of P in fp32.
 
 #include <hip/hip_runtime.h>
 #include <math.h>

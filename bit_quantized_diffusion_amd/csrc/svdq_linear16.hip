@@ -9,9 +9,9 @@
 // results lie along n, the dense dimension of y.
 //
 // Measured (passes over changing inputs, bf16): 4608 x 3072 -> 12288 with GELU
-// 292 us (1190 TFLOP/s), 4608 x 3072 -> 3072 with gate and residual 71 us (1220
-// TFLOP/s), both at the chip's power limit; 2 x 3072 -> 18432 22.2 us (5.1
-// TB/s), bound by reading W; fp16 333 x 4096 -> 3072 19.4 us (430 TFLOP/s),
+// 300 us (1160 TFLOP/s), 4608 x 3072 -> 3072 with gate and residual 75 us (1150
+// TFLOP/s), both at the chip's power limit; 2 x 3072 -> 18432 22.4 us (5.1
+// TB/s), bound by reading W; fp16 333 x 4096 -> 3072 20 us (415 TFLOP/s),
 // bound by the operands' way from L2.
 
 #include <hip/hip_runtime.h>
