@@ -27,7 +27,7 @@
 // even for the matrix core and l sums the unrounded values.
 //
 // Measured (passes over changing inputs, bf16): 4608 tokens x 24 heads of 128
-// 247 to 255 us over boxes (1060 to 1020 TFLOP/s), bound by power (the same
+// 247 to 255 us from card to card (1060 to 1020 TFLOP/s), bound by power (the same
 // loop on zeros runs at 1470); one token of each of 8 caches of 0 to 16384
 // keys, 8 key heads, 56 us (4.3 TB/s), bound by reading K and V; 77 tokens x
 // 12 heads of 64 in fp16, 5.2 us on the device, bound by its launch.  P in 16

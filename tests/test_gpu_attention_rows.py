@@ -95,8 +95,8 @@ def test_queries_that_no_sequence_holds(lens_q, lens_k, hq, hk, d, causal, front
     for ws in (torch.full((max(size, 16),), 0x42, dtype=torch.uint8, device="cuda"), None):
         print("padding", lens_q[:5], lens_k[:5], hq, hk, d, causal, front, back, ws is None, flush=True)
         out = torch.full_like(q, 7.0)
-        del_me = torch.full((q.shape[0], hq), 7.0, device="cuda")   # what a new lse may lie in
-        del del_me
+        stale = torch.full((q.shape[0], hq), 7.0, device="cuda")   # what a new lse may lie in
+        del stale
         o, lse = bq.attention(q, k, v, cu_seqlens_q=cu_q, cu_seqlens_k=cu_k, causal=causal, return_lse=True, workspace=ws, out=out)
         assert_within(o[front:front + n], want, bo, "o")
         assert_within(lse[front:front + n], want_lse, bl, "lse")
