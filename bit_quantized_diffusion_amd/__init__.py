@@ -24,7 +24,9 @@ from ._lib import (BF16, F16, INT4, MXFP4, SVDQ_ERR_HIP, SVDQ_ERR_INVALID_ARG,  
                    SVDQ_ERR_SHAPE, SVDQ_ERR_UNSUPPORTED_DEVICE, SVDQ_OK,
                    EXPORTED, LIB_PATH, SvdqError, check, lib, status_string)
 from .block_ops import (attention, attention_workspace_size, layer_norm, linear16,  # noqa: F401
-                        linear16_workspace_size)
+                        linear16_workspace_size, rms_norm)
+from .fp8_ops import (FP8_BLOCK, gemm_fp8, gemm_fp8_workspace_size, linear_fp8, pack_fp8,  # noqa: F401
+                      quantize_fp8, rms_norm_fp8)
 
 __all__ = [
     "INT4", "MXFP4", "SvdqError", "lib", "LIB_PATH", "status_string", "merge_lora",
@@ -34,7 +36,8 @@ __all__ = [
     "PackedLinear", "linear", "gemm_w4a4_lora_up_gelu", "mlp_gemm_gelu_quant", "mlp",
     "pack_w4a16", "gemm_w4a16", "mfma_ceiling",
     "BF16", "F16", "attention", "attention_workspace_size", "linear16",
-    "linear16_workspace_size", "layer_norm",
+    "linear16_workspace_size", "layer_norm", "rms_norm",
+    "FP8_BLOCK", "pack_fp8", "quantize_fp8", "rms_norm_fp8", "gemm_fp8", "gemm_fp8_workspace_size", "linear_fp8",
 ]
 
 

@@ -41,7 +41,7 @@ else:
         (lambda device: torch.cuda.current_stream(device).cuda_stream)
     _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _block_ops.setup(torch.Tensor, torch.bfloat16, torch.float16, torch.float32, torch.uint8, torch.int32, _raw_stream,
-                     _current_device, torch.cuda.set_device, check)
+                     _current_device, torch.cuda.set_device, check, torch.float8_e4m3fn, torch.int8)
 
 
 def attention_workspace_size(total_q: int, total_k: int, batch: int, heads_q: int, heads_k: int, head_dim: int) -> int:
@@ -111,3 +111,14 @@ def layer_norm(x, weight=None, bias=None, *, scale=None, shift=None, group_rows=
     r // group_rows (group_rows defaults to M / groups).  Rows may be
     strided.  `out` may be x.  No gradient."""
     return _block_ops.layer_norm(x, weight, bias, scale, shift, group_rows, eps, out)
+
+
+def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, out=None, residual_out=None):
+    """Root-mean-square norm over the last dimension of h = x [+ residual]:
+    h / sqrt(mean(h^2) + eps) [* weight], fp32 arithmetic, one rounding.
+
+    x and residual [M][K], weight [K].  Rows may be strided.  Returns y, or
+    with a residual (y, h): h is the sum, rounded once (y is taken from the
+    unrounded one).  `out` may be x or residual, and so may `residual_out`,
+    but not both the same.  No gradient."""
+    return _block_ops.rms_norm(x, weight, residual, eps, out, residual_out, False)

@@ -73,6 +73,19 @@ int check_linear16_shape(int M, int N, int K) {
   return SVDQ_OK;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// codes of 8 bits: whole 16-byte chunks in a row, 256 rows of a tile in 31 bits
+int check_codes(int K) { return K < 16 || K % 16 || K > 1 << 22 ? SVDQ_ERR_SHAPE : SVDQ_OK; }
+
+int check_gemm_fp8_shape(int M, int N, int K) {
+  if (M < 1 || N < 1 || M > kMostRows || N > (1 << 28) - 32) return SVDQ_ERR_SHAPE;
+  // a launch holds less than 2^32 threads: 256 for a tile of 64 x 64 or more,
+  // or for 16 channels of few rows
+  if (((M + 63LL) / 64) * ((N + 63LL) / 64) >= 1LL << 24) return SVDQ_ERR_SHAPE;
+  return check_codes(K);
+}
+
 int hip_status(int e) { return e == 0 ? SVDQ_OK : SVDQ_ERR_HIP; }
 
 }  // namespace
@@ -416,6 +429,59 @@ int svdq_layer_norm(const void* x, int64_t ldx, const void* weight, const void* 
                                            ldy, M, K, eps, dtype, stream));
 }
 
+int svdq_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, void* sum,
+                  int64_t ld_sum, void* y, int64_t ldy, uint8_t* yq, float* ys, int M, int K, float eps, int dtype,
+                  void* stream) {
+  int st = check_dtype(dtype);
+  if (st) return st;
+  if (!x || !yq != !ys || !y == !yq) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned2(x) || !aligned2(residual) || !aligned2(weight) || !aligned2(sum) || !aligned2(y) || !aligned16(yq) ||
+      !aligned4(ys))
+    return SVDQ_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || std::isinf(eps)) return SVDQ_ERR_INVALID_ARG;
+  if (M < 1 || M > kMostRows || K < 1 || K > 65536 || (yq && K % 16)) return SVDQ_ERR_SHAPE;
+  if (ldx < K || (residual && ldr < K) || (sum && ld_sum < K) || (y && ldy < K)) return SVDQ_ERR_SHAPE;
+  if ((st = current_device_ok())) return st;
+  return hip_status(svdq_launch_rms_norm(x, ldx, residual, ldr, weight, sum, ld_sum, y, ldy, yq, ys, M, K, eps, dtype, stream));
+}
+
+int svdq_quantize_fp8(const void* x, int64_t ldx, uint8_t* xq, float* xs, int M, int K, int dtype, void* stream) {
+  int st = check_dtype(dtype);
+  if (st) return st;
+  if (!x || !xq || !xs || !aligned2(x) || !aligned16(xq) || !aligned4(xs)) return SVDQ_ERR_INVALID_ARG;
+  if ((st = check_codes(K))) return st;
+  if (M < 1 || M > kMostRows || ldx < K) return SVDQ_ERR_SHAPE;
+  if ((st = current_device_ok())) return st;
+  return hip_status(svdq_launch_quantize_fp8(x, ldx, xq, xs, M, K, dtype, stream));
+}
+
+int svdq_gemm_fp8_workspace_size(int M, int N, int K, size_t* out_bytes) {
+  if (!out_bytes) return SVDQ_ERR_INVALID_ARG;
+  *out_bytes = 0;
+  const int st = check_gemm_fp8_shape(M, N, K);
+  if (st) return st;
+  *out_bytes = svdq_gemm_fp8_plan_bytes(M, N, K);
+  return SVDQ_OK;
+}
+
+int svdq_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const void* bias, const void* gate,
+                  int64_t ld_gate, int group_rows, const void* residual, int64_t ldr, void* y, int64_t ldy, int M, int N,
+                  int K, int activation, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_dtype(dtype);
+  if (st) return st;
+  if (activation != SVDQ_ACT_NONE && activation != SVDQ_ACT_GELU && activation != SVDQ_ACT_SILU)
+    return SVDQ_ERR_INVALID_ARG;
+  if ((st = check_gemm_fp8_shape(M, N, K))) return st;
+  if (!xq || !xs || !wq || !ws || !y) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(xq) || !aligned4(xs) || !aligned16(wq) || !aligned4(ws) || !aligned2(y) || !aligned2(bias) ||
+      !aligned2(gate) || !aligned2(residual) || !aligned16(workspace))
+    return SVDQ_ERR_INVALID_ARG;
+  if (ldy < N || (residual && ldr < N) || (gate && (ld_gate < N || group_rows < 1))) return SVDQ_ERR_SHAPE;
+  if ((st = current_device_ok())) return st;
+  return hip_status(svdq_launch_gemm_fp8(xq, xs, wq, ws, bias, gate, ld_gate, group_rows < 1 ? 1 : group_rows, residual, ldr,
+                                         y, ldy, M, N, K, activation, dtype, workspace, workspace_bytes, stream));
+}
+
 int svdq_bench_mfma_ceiling(int precision, int blocks, int iters, float* out, void* stream) {
   if (!out || !aligned16(out)) return SVDQ_ERR_INVALID_ARG;
   if (precision != SVDQ_INT4 && precision != SVDQ_MXFP4) return SVDQ_ERR_INVALID_ARG;
@@ -454,6 +520,14 @@ int svdq_debug_linear16_plan(int M, int N, int K, int aligned, int32_t* plan) {
   if (st) return st;
   if (aligned && K % 8) return SVDQ_ERR_SHAPE;
   svdq_linear16_plan(M, N, K, aligned, plan);
+  return SVDQ_OK;
+}
+
+int svdq_debug_gemm_fp8_plan(int M, int N, int K, int32_t* plan) {
+  if (!plan) return SVDQ_ERR_INVALID_ARG;
+  const int st = check_gemm_fp8_shape(M, N, K);
+  if (st) return st;
+  svdq_gemm_fp8_plan(M, N, K, plan);
   return SVDQ_OK;
 }
 

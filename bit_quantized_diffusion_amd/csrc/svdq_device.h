@@ -1,6 +1,6 @@
-// Device helpers shared by the 16-bit operators (attention, linear16, layer
-// norm): element types, buffer descriptors, loads that go straight to LDS,
-// waits.  gfx950 only.
+// Device helpers shared by the 16-bit operators (attention, linear16, norms)
+// and the 8-bit ones: element types, buffer descriptors, loads that go
+// straight to LDS, waits.  gfx950 only.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -15,6 +15,7 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef int v8i __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
@@ -87,6 +88,12 @@ __device__ __forceinline__ void dma_b128(__amdgpu_buffer_rsrc_t r, uint32_t lds,
 __device__ __forceinline__ void dma_b128(__amdgpu_buffer_rsrc_t r, uint32_t lds, int voff, int soff) {
   asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                :: "v"(voff), "s"(r), "s"(soff), "{m0}"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
+}
+
+// 4 bytes per lane, to lds + 4 lane
+__device__ __forceinline__ void dma_b32(__amdgpu_buffer_rsrc_t r, uint32_t lds, int voff) {
+  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :: "v"(voff), "s"(r), "{m0}"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
 }
 
 // at most N of the wave's vector-memory loads outstanding
@@ -173,6 +180,15 @@ __device__ __forceinline__ void unpack8(v4u v, float (&f)[8]) {
 template <typename E>
 __device__ __forceinline__ v4u pack8(const float (&f)[8]) {
   return v4u{E::pack2(f[0], f[1]), E::pack2(f[2], f[3]), E::pack2(f[4], f[5]), E::pack2(f[6], f[7])};
+}
+
+// 8-bit codes, e4m3: largest value 448, no infinity, NaN 0x7F.  Four fp32
+// values to the bytes of a word, rounded to nearest even; past 448 and half a
+// step they give NaN, so callers scale or clamp first.
+constexpr float kMostF8 = 448.f;
+__device__ __forceinline__ uint32_t pack4_f8(float a, float b, float c, float d) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true));
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }

@@ -98,6 +98,16 @@ int svdq_launch_linear16(const void* x, int64_t ldx, const void* w, int64_t ldw,
 int svdq_launch_layer_norm(const void* x, int64_t ldx, const void* weight, const void* bias, const void* scale,
                            const void* shift, int64_t ld_mod, int group_rows, void* y, int64_t ldy, int M, int K,
                            float eps, int dtype, void* stream);
+int svdq_launch_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, void* sum,
+                         int64_t ld_sum, void* y, int64_t ldy, uint8_t* yq, float* ys, int M, int K, float eps, int dtype,
+                         void* stream);
+int svdq_launch_quantize_fp8(const void* x, int64_t ldx, uint8_t* xq, float* xs, int M, int K, int dtype, void* stream);
+size_t svdq_gemm_fp8_plan_bytes(int M, int N, int K);
+void svdq_gemm_fp8_plan(int M, int N, int K, int32_t* plan);
+int svdq_launch_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const void* bias,
+                         const void* gate, int64_t ld_gate, int group_rows, const void* residual, int64_t ldr, void* y,
+                         int64_t ldy, int M, int N, int K, int activation, int dtype, void* workspace,
+                         size_t workspace_bytes, void* stream);
 int svdq_launch_mfma_ceiling(int precision, int blocks, int iters, float* out, void* stream);
 int svdq_launch_unfused_linear_noalloc(const void* x, int M, int K, const float* smooth_inv, const void* lora_down,
                                        int rank, const uint8_t* wq, const void* ws, const void* lora_up,

@@ -186,7 +186,200 @@ int launch(const NormArgs& a, hipStream_t stream) {
   return static_cast<int>(hipGetLastError());
 }
 
+// ---------------------------------------------------------------------------
+// Root-mean-square norm with the residual's addition:
+//
+//   h = x [+ residual],  y = h rstd [* w],  rstd = 1 / sqrt(mean(h^2) + eps)
+//
+// h is held in fp32 between the sum, the norm and its own store (rounded
+// once).  y is rounded to 16 bits, or (FP8) to e4m3 codes with a scale for each
+// 128 values of the row: s = max(amax, 2^-100) / 448, code = e4m3(y * (1 / s)).
+// A block of 128 is 16 consecutive lanes, so its largest magnitude is four
+// exchanges.  A NaN stays one; an infinity makes its block's scale infinite
+// and its codes 0 and NaN.  Memory-bound like the layer norm above.
+// ---------------------------------------------------------------------------
+
+struct RmsArgs {
+  const uint16_t *x, *residual, *weight;
+  uint16_t *sum, *y;
+  uint8_t* yq;
+  float* ys;        // [blocks of 128][M]
+  int64_t ldx, ldr, ld_sum, ldy;
+  int M, K;
+  float eps;
+};
+
+// The codes of a lane's 8 values, whose block of 128 its 16 lanes hold; the
+// first of them stores the scale.
+__device__ __forceinline__ void store_codes(const float (&f)[8], uint8_t* codes, float* scale, int k, int K) {
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+#pragma unroll
+  for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  const float s = fmaxf(top, 0x1p-100f) / kMostF8, inv = 1.f / s;
+  if (k >= K) return;
+  v2u q;
+  q[0] = pack4_f8(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+  q[1] = pack4_f8(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+  *reinterpret_cast<v2u*>(codes) = q;
+  if ((k & 127) == 0) *scale = s;
+}
+
+template <typename E, int LANES, int WAVES, int CHUNKS, bool TAIL, bool FP8>
+__global__ __launch_bounds__(WAVES > 1 ? WAVES * 64 : 256) void k_rms_norm(RmsArgs a) {
+  static_assert(WAVES == 1 || LANES == 64, "several waves take whole rows");
+  static_assert(!FP8 || (LANES >= 16 && !TAIL), "a block's lanes stand beside each other");
+  constexpr int kThreads = WAVES * LANES;                  // threads of a row
+  constexpr int kRows = WAVES > 1 ? 1 : 256 / LANES;       // rows of a workgroup
+  __shared__ float sums[WAVES];
+  const int t = threadIdx.x % kThreads;
+  const int64_t row = (static_cast<int64_t>(blockIdx.y) * kGridX + blockIdx.x) * kRows + threadIdx.x / kThreads;
+  if (row >= a.M) return;   // whole rows' lanes leave together
+  const uint16_t* const x = a.x + row * a.ldx;
+  v4u raw[CHUNKS], more[CHUNKS];
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) raw[c] = row_chunk<TAIL>(x, (c * kThreads + t) * 8, a.K);
+  if (a.residual) {
+    const uint16_t* const r = a.residual + row * a.ldr;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) more[c] = row_chunk<TAIL>(r, (c * kThreads + t) * 8, a.K);
+  }
+  float f[CHUNKS][8];
+  float square = 0.f;
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    const bool in = (c * kThreads + t) * 8 < a.K;
+    unpack8<E>(in ? raw[c] : v4u{0, 0, 0, 0}, f[c]);
+    if (a.residual) {
+      float r[8];
+      unpack8<E>(in ? more[c] : v4u{0, 0, 0, 0}, r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[c][e] += r[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) square += f[c][e] * f[c][e];
+  }
+  const float rstd = 1.f / sqrtf(row_total<LANES, WAVES>(square, sums) * (1.f / a.K) + a.eps);
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    const int k = (c * kThreads + t) * 8;
+    if (!FP8 && k >= a.K) break;
+    if (a.sum && k < a.K) {
+      uint16_t* const p = a.sum + row * a.ld_sum + k;
+      if (!TAIL || k + 8 <= a.K)
+        stream8(p, pack8<E>(f[c]));
+      else
+        store8(p, pack8<E>(f[c]), a.K - k);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[c][e] *= rstd;
+    if (a.weight) {
+      float w[8];
+      unpack8<E>(row_chunk<TAIL>(a.weight, k, a.K), w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[c][e] *= w[e];
+    }
+    if constexpr (FP8) {
+      if (k >= a.K)   // past the row: the block's other lanes still exchange
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[c][e] = 0.f;
+      store_codes(f[c], a.yq + row * a.K + k, a.ys + static_cast<int64_t>(k >> 7) * a.M + row, k, a.K);
+    } else if (!TAIL || k + 8 <= a.K) {
+      stream8(a.y + row * a.ldy + k, pack8<E>(f[c]));
+    } else {
+      store8(a.y + row * a.ldy + k, pack8<E>(f[c]), a.K - k);
+    }
+  }
+}
+
+template <typename E, bool FP8, int LANES, int WAVES, int CHUNKS>
+void start_rms(const RmsArgs& a, hipStream_t stream) {
+  constexpr int kRows = WAVES > 1 ? 1 : 256 / LANES;
+  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(a.M) + kRows - 1) / kRows);
+  const dim3 grid(blocks < kGridX ? blocks : kGridX, (blocks + kGridX - 1) / kGridX);
+  constexpr int kBlock = WAVES > 1 ? WAVES * 64 : 256;
+  if constexpr (FP8) {
+    k_rms_norm<E, LANES, WAVES, CHUNKS, false, true><<<grid, kBlock, 0, stream>>>(a);
+  } else if (a.K % 8) {
+    k_rms_norm<E, LANES, WAVES, CHUNKS, true, false><<<grid, kBlock, 0, stream>>>(a);
+  } else {
+    k_rms_norm<E, LANES, WAVES, CHUNKS, false, false><<<grid, kBlock, 0, stream>>>(a);
+  }
+}
+
+template <typename E, bool FP8>
+int launch_rms(const RmsArgs& a, hipStream_t stream) {
+  const int chunks = (a.K + 7) / 8;
+  if (chunks <= 16)
+    start_rms<E, FP8, 16, 1, 1>(a, stream);
+  else if (chunks <= 64)
+    start_rms<E, FP8, 64, 1, 1>(a, stream);
+  else if (chunks <= 128)
+    start_rms<E, FP8, 64, 1, 2>(a, stream);
+  else if (chunks <= 256)
+    start_rms<E, FP8, 64, 1, 4>(a, stream);
+  else if (chunks <= 512)
+    start_rms<E, FP8, 64, 1, 8>(a, stream);
+  else if (chunks <= 1024)
+    start_rms<E, FP8, 64, 4, 4>(a, stream);
+  else if (chunks <= 2048)
+    start_rms<E, FP8, 64, 4, 8>(a, stream);
+  else
+    start_rms<E, FP8, 64, 16, 8>(a, stream);
+  return static_cast<int>(hipGetLastError());
+}
+
+// Codes and scales of a matrix: 16 lanes a block of 128 values.
+template <typename E>
+__global__ __launch_bounds__(256) void k_quantize8(const uint16_t* x, int64_t ldx, uint8_t* xq, float* xs, int M, int K) {
+  const int blocks = (K + 127) / 128;
+  const int64_t i = (static_cast<int64_t>(blockIdx.y) * kGridX + blockIdx.x) * 16 + (threadIdx.x >> 4);
+  const int64_t row = i / blocks;
+  if (row >= M) return;   // a block's lanes leave together
+  const int g = static_cast<int>(i - row * blocks), k = g * 128 + (threadIdx.x & 15) * 8;
+  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (k < K) unpack8<E>(load8(x + row * ldx + k), f);
+  store_codes(f, xq + row * K + k, xs + static_cast<int64_t>(g) * M + row, k, K);
+}
+
 }  // namespace
+
+extern "C" int svdq_launch_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                                    void* sum, int64_t ld_sum, void* y, int64_t ldy, uint8_t* yq, float* ys, int M, int K,
+                                    float eps, int dtype, void* stream) {
+  RmsArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.weight = static_cast<const uint16_t*>(weight);
+  a.sum = static_cast<uint16_t*>(sum);
+  a.y = static_cast<uint16_t*>(y);
+  a.yq = yq;
+  a.ys = ys;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.ld_sum = ld_sum;
+  a.ldy = ldy;
+  a.M = M;
+  a.K = K;
+  a.eps = eps;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (yq) return dtype == SVDQ_BF16 ? launch_rms<Bf16, true>(a, s) : launch_rms<F16, true>(a, s);
+  return dtype == SVDQ_BF16 ? launch_rms<Bf16, false>(a, s) : launch_rms<F16, false>(a, s);
+}
+
+extern "C" int svdq_launch_quantize_fp8(const void* x, int64_t ldx, uint8_t* xq, float* xs, int M, int K, int dtype,
+                                        void* stream) {
+  const int64_t groups = (static_cast<int64_t>((K + 127) / 128) * M + 15) / 16;
+  const dim3 grid(static_cast<unsigned>(groups < kGridX ? groups : kGridX), static_cast<unsigned>((groups + kGridX - 1) / kGridX));
+  const uint16_t* const p = static_cast<const uint16_t*>(x);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (dtype == SVDQ_BF16)
+    k_quantize8<Bf16><<<grid, 256, 0, s>>>(p, ldx, xq, xs, M, K);
+  else
+    k_quantize8<F16><<<grid, 256, 0, s>>>(p, ldx, xq, xs, M, K);
+  return static_cast<int>(hipGetLastError());
+}
 
 extern "C" int svdq_launch_layer_norm(const void* x, int64_t ldx, const void* weight, const void* bias, const void* scale,
                                       const void* shift, int64_t ld_mod, int group_rows, void* y, int64_t ldy, int M,

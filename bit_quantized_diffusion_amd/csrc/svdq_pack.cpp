@@ -630,3 +630,47 @@ extern "C" int svdq_pack_w4a16(const uint16_t* w_bf16, int K, int N, uint8_t* wq
   }, 16);
   return SVDQ_OK;
 }
+
+namespace {
+
+// fp32 to e4m3, nearest even: 3 bits of fraction, exponents from 2^-6 (below
+// it steps of 2^-9), NaN 0x7F past 448 and half a step
+uint8_t f32_to_e4m3(float f) {
+  const uint8_t sign = std::signbit(f) ? 0x80 : 0;
+  const float a = std::fabs(f);
+  if (!(a < 464.f)) return sign | (a == 464.f ? 0x7E : 0x7F);
+  int e = -5;
+  if (a >= 0x1p-6f) std::frexp(a, &e);   // a = m 2^e with m in [1/2, 1)
+  const int steps = static_cast<int>(std::nearbyint(std::ldexp(a, 4 - e)));   // of 2^(e - 4): 8 to 16, below 2^-6 0 to 8
+  return sign | static_cast<uint8_t>((e + 5) * 8 + steps);   // a carry past 16 steps is the next exponent
+}
+
+}  // namespace
+
+// One scale for each 128 x 128 values of a weight.
+extern "C" int svdq_pack_fp8(const uint16_t* w, int K, int N, int dtype, uint8_t* wq, float* ws) {
+  if (!w || !wq || !ws || (dtype != SVDQ_BF16 && dtype != SVDQ_F16)) return SVDQ_ERR_INVALID_ARG;
+  if (N < 1 || K < 16 || K % 16 || K > 1 << 22) return SVDQ_ERR_SHAPE;
+  const int64_t blocks_k = (K + SVDQ_FP8_BLOCK - 1) / SVDQ_FP8_BLOCK, blocks_n = (static_cast<int64_t>(N) + SVDQ_FP8_BLOCK - 1) / SVDQ_FP8_BLOCK;
+  parallel_for(blocks_n, [&](int64_t bn) {
+    const int64_t n0 = bn * SVDQ_FP8_BLOCK, n1 = std::min<int64_t>(n0 + SVDQ_FP8_BLOCK, N);
+    for (int64_t g = 0; g < blocks_k; ++g) {
+      const int64_t k0 = g * SVDQ_FP8_BLOCK, k1 = std::min<int64_t>(k0 + SVDQ_FP8_BLOCK, K);
+      auto value = [&](int64_t n, int64_t k) {
+        const uint16_t b = w[n * K + k];
+        return dtype == SVDQ_BF16 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b);
+      };
+      float top = 0x1p-100f;
+      for (int64_t n = n0; n < n1; ++n)
+        for (int64_t k = k0; k < k1; ++k) {
+          const float a = std::fabs(value(n, k));
+          if (a > top) top = a;
+        }
+      const float s = top / 448.f, inv = 1.f / s;
+      ws[bn * blocks_k + g] = s;
+      for (int64_t n = n0; n < n1; ++n)
+        for (int64_t k = k0; k < k1; ++k) wq[n * K + k] = f32_to_e4m3(value(n, k) * inv);
+    }
+  });
+  return SVDQ_OK;
+}

@@ -1,4 +1,4 @@
-// Python side of the 16-bit block operators: argument checks, output and
+// Python side of the 16-bit and 8-bit block operators: argument checks, output and
 // workspace tensors, the device and the stream of a call.
 //
 // The smallest calls take longer on the host than on the device.  With the
@@ -19,7 +19,7 @@
 namespace {
 
 // set once by setup(): torch's Tensor, dtypes and functions
-PyObject *g_tensor, *g_bf16, *g_f16, *g_f32, *g_u8, *g_i32, *g_stream, *g_current, *g_set_device, *g_check;
+PyObject *g_tensor, *g_bf16, *g_f16, *g_f32, *g_u8, *g_i32, *g_stream, *g_current, *g_set_device, *g_check, *g_f8, *g_i8;
 PyObject *s_dtype, *s_shape, *s_stride, *s_get_device, *s_data_ptr, *s_new_empty, *s_is_contiguous, *s_numel;
 PyObject* s_kw_dtype;   // ("dtype",)
 
@@ -489,9 +489,189 @@ PyObject* layer_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return out.release();
 }
 
-// setup(Tensor, bfloat16, float16, float32, uint8, int32, current stream, current device, set device, check)
+// A contiguous tensor of this dtype, shape and device.
+bool exactly(PyObject* o, PyObject* dtype, long device, int dims, int64_t a, int64_t b, int64_t c, const char* name, Tensor& t) {
+  if (!read(o, t)) return no_tensor(name, "");
+  if (t.dtype != dtype || t.device != device || device < 0) {
+    PyErr_Format(PyExc_TypeError, "%s: expected %S on cuda:%ld, got %S on device %ld", name, dtype, device, t.dtype, t.device);
+    return false;
+  }
+  if (!shaped(o, t, dims, a, b, c, name)) return false;
+  int64_t dense = 1;
+  for (int i = dims - 1; i >= 0; --i) {
+    if (t.shape[i] > 1 && t.stride[i] != dense) {
+      PyErr_Format(PyExc_ValueError, "%s: must be contiguous", name);
+      return false;
+    }
+    dense *= t.shape[i];
+  }
+  return true;
+}
+
+int64_t blocks_of(int64_t n) { return (n + SVDQ_FP8_BLOCK - 1) / SVDQ_FP8_BLOCK; }
+
+void* pointer_of(PyObject* o) {
+  Ref ptr(PyObject_CallMethodNoArgs(o, s_data_ptr));
+  return ptr ? PyLong_AsVoidPtr(ptr.get()) : nullptr;
+}
+
+// rms_norm(x, weight, residual, eps, out, residual_out, codes) -> y or (codes, scales), and h with a residual
+PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!count_of("rms_norm", n, 7)) return nullptr;
+  Tensor x, weight, residual, sum, y;
+  int code;
+  if (!operand(args[0], 2, "x", "[M][K]", x, code)) return nullptr;
+  const int64_t M = x.shape[0], K = x.shape[1];
+  if (!countable({M, K}, "rms_norm")) return nullptr;
+  const int codes = PyObject_IsTrue(args[6]);
+  if (codes < 0) return nullptr;
+  if (args[1] != Py_None && !like(args[1], x, 1, K, 0, 0, "weight", weight)) return nullptr;
+  if (args[2] != Py_None && !like(args[2], x, 2, M, K, 0, "residual", residual)) return nullptr;
+  const double eps = PyFloat_AsDouble(args[3]);
+  if (eps == -1.0 && PyErr_Occurred()) return nullptr;
+  if (args[5] != Py_None && args[2] == Py_None) {
+    PyErr_SetString(PyExc_ValueError, "residual_out without residual");
+    return nullptr;
+  }
+  Ref out, scales, h;
+  void *yq = nullptr, *ys = nullptr;
+  if (codes) {
+    if (K % 16) {
+      PyErr_Format(PyExc_ValueError, "x: rows of codes take multiples of 16 values, got %lld", static_cast<long long>(K));
+      return nullptr;
+    }
+    out.reset(new_empty(args[0], {M, K}, g_f8));
+    if (out) scales.reset(new_empty(args[0], {blocks_of(K), M}, g_f32));
+    if (!out || !scales) return nullptr;
+    yq = pointer_of(out.get());
+    ys = pointer_of(scales.get());
+  } else {
+    out.reset(output(args[4], args[0], x, 2, M, K, 0, y));
+    if (!out) return nullptr;
+  }
+  if (residual.ptr || args[2] != Py_None) {
+    if (args[5] != Py_None) {
+      if (!like(args[5], x, 2, M, K, 0, "residual_out", sum)) return nullptr;
+      Py_INCREF(args[5]);
+      h.reset(args[5]);
+    } else {
+      h.reset(output(Py_None, args[0], x, 2, M, K, 0, sum));
+      if (!h) return nullptr;
+    }
+  }
+  if (M && !run(x.device, [&](void* stream) {
+        return svdq_rms_norm(x.ptr, x.ld(), residual.ptr, residual.ptr ? residual.ld() : 0, weight.ptr, sum.ptr,
+                             sum.ptr ? sum.ld() : 0, y.ptr, y.ptr ? y.ld() : 0, static_cast<uint8_t*>(yq),
+                             static_cast<float*>(ys), static_cast<int>(M), static_cast<int>(K), static_cast<float>(eps), code,
+                             stream);
+      }))
+    return nullptr;
+  if (codes) return h ? PyTuple_Pack(3, out.get(), scales.get(), h.get()) : PyTuple_Pack(2, out.get(), scales.get());
+  return h ? PyTuple_Pack(2, out.get(), h.get()) : out.release();
+}
+
+// quantize_fp8(x) -> (codes, scales)
+PyObject* quantize_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!count_of("quantize_fp8", n, 1)) return nullptr;
+  Tensor x;
+  int code;
+  if (!operand(args[0], 2, "x", "[M][K]", x, code)) return nullptr;
+  const int64_t M = x.shape[0], K = x.shape[1];
+  if (!countable({M, K}, "quantize_fp8")) return nullptr;
+  Ref xq(new_empty(args[0], {M, K}, g_f8)), xs(new_empty(args[0], {blocks_of(K), M}, g_f32));
+  if (!xq || !xs) return nullptr;
+  void *q = pointer_of(xq.get()), *s = pointer_of(xs.get());
+  if (M && !run(x.device, [&](void* stream) {
+        return svdq_quantize_fp8(x.ptr, x.ld(), static_cast<uint8_t*>(q), static_cast<float*>(s), static_cast<int>(M),
+                                 static_cast<int>(K), code, stream);
+      }))
+    return nullptr;
+  return PyTuple_Pack(2, xq.get(), xs.get());
+}
+
+// gemm_fp8(xq, xs, wq, ws, bias, activation code, gate, residual, group_rows, dtype, out, workspace), and with
+// xs None, xq being 16-bit activations: their codes are made first
+PyObject* gemm_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!count_of("gemm_fp8", n, 12)) return nullptr;
+  Tensor x, xs, wq, ws, bias, residual, y, like_y;
+  int code;
+  const bool whole = args[1] == Py_None;
+  if (whole) {
+    if (!operand(args[0], 2, "x", "[M][K]", x, code)) return nullptr;
+  } else {
+    if (args[9] != g_bf16 && args[9] != g_f16) {
+      PyErr_SetString(PyExc_ValueError, "dtype: expected torch.bfloat16 or torch.float16");
+      return nullptr;
+    }
+    code = args[9] == g_bf16 ? SVDQ_BF16 : SVDQ_F16;
+    if (!read(args[0], x)) {
+      no_tensor("xq", "[M][K]");
+      return nullptr;
+    }
+    if (x.dims != 2 || x.device < 0) {
+      no_tensor("xq", "[M][K]");
+      return nullptr;
+    }
+  }
+  const int64_t M = x.shape[0], K = x.shape[1];
+  if (!read(args[2], wq) || wq.dims != 2) {
+    no_tensor("wq", "[N][K]");
+    return nullptr;
+  }
+  const int64_t N = wq.shape[0];
+  if (!countable({M, N, K}, "gemm_fp8")) return nullptr;
+  if (!whole && (!exactly(args[0], g_f8, x.device, 2, M, K, 0, "xq", x) ||
+                 !exactly(args[1], g_f32, x.device, 2, blocks_of(K), M, 0, "xs", xs)))
+    return nullptr;
+  if (!exactly(args[2], g_f8, x.device, 2, N, K, 0, "wq", wq) ||
+      !exactly(args[3], g_f32, x.device, 2, blocks_of(N), blocks_of(K), 0, "ws", ws))
+    return nullptr;
+  like_y.dtype = code == SVDQ_BF16 ? g_bf16 : g_f16;
+  like_y.device = x.device;
+  const long act = PyLong_AsLong(args[5]);
+  if (act == -1 && PyErr_Occurred()) return nullptr;
+  if (args[4] != Py_None && !like(args[4], like_y, 1, N, 0, 0, "bias", bias)) return nullptr;
+  Grouped gate;
+  if (args[6] != Py_None && !grouped(args[6], like_y, M, N, args[8], "gate", gate)) return nullptr;
+  if (args[7] != Py_None && !like(args[7], like_y, 2, M, N, 0, "residual", residual)) return nullptr;
+  Ref out;
+  if (args[10] != Py_None || whole) {
+    out.reset(output(args[10], args[0], like_y, 2, M, N, 0, y));
+  } else {
+    out.reset(new_empty(args[0], {M, N}, like_y.dtype));
+    if (out && !read(out.get(), y)) return nullptr;
+  }
+  if (!out) return nullptr;
+  if (M == 0) return out.release();
+  const int m = static_cast<int>(M), nn = static_cast<int>(N), k = static_cast<int>(K);
+  size_t bytes = 0, size;
+  if (args[11] != Py_None && !fine(svdq_gemm_fp8_workspace_size(m, nn, k, &bytes))) return nullptr;
+  void* space;
+  Ref keep, codes;
+  if (!workspace_of(args[11], args[0], x, bytes, space, size, keep)) return nullptr;
+  uint8_t* q = static_cast<uint8_t*>(x.ptr);
+  float* s = static_cast<float*>(xs.ptr);
+  if (whole) {
+    // codes and scales in one piece; K is a multiple of 16, or the first call refuses it
+    codes.reset(new_empty(args[0], {(M * K + 15) / 16 * 16 + 4 * M * blocks_of(K)}, g_u8));
+    if (!codes) return nullptr;
+    q = static_cast<uint8_t*>(pointer_of(codes.get()));
+    s = reinterpret_cast<float*>(q + (M * K + 15) / 16 * 16);
+  }
+  if (!run(x.device, [&](void* stream) {
+        if (whole)
+          if (const int st = svdq_quantize_fp8(x.ptr, x.ld(), q, s, m, k, code, stream)) return st;
+        return svdq_gemm_fp8(q, s, static_cast<uint8_t*>(wq.ptr), static_cast<float*>(ws.ptr), bias.ptr, gate.ptr, gate.ld,
+                             static_cast<int>(gate.rows), residual.ptr, residual.ptr ? residual.ld() : 0, y.ptr, y.ld(), m,
+                             nn, k, static_cast<int>(act), code, space, size, stream);
+      }))
+    return nullptr;
+  return out.release();
+}
+
+// setup(Tensor, bfloat16, float16, float32, uint8, int32, current stream, current device, set device, check, e4m3, int8)
 PyObject* setup(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  PyObject** const to[] = {&g_tensor, &g_bf16, &g_f16, &g_f32, &g_u8, &g_i32, &g_stream, &g_current, &g_set_device, &g_check};
+  PyObject** const to[] = {&g_tensor, &g_bf16, &g_f16, &g_f32, &g_u8, &g_i32, &g_stream, &g_current, &g_set_device, &g_check, &g_f8, &g_i8};
   constexpr Py_ssize_t kCount = sizeof(to) / sizeof(to[0]);
   if (!count_of("setup", n, kCount)) return nullptr;
   if (!PyType_Check(args[0])) {
@@ -523,6 +703,9 @@ PyMethodDef g_methods[] = {
     {"attention", entry<ready<attention>>(), METH_FASTCALL, nullptr},
     {"linear16", entry<ready<linear16>>(), METH_FASTCALL, nullptr},
     {"layer_norm", entry<ready<layer_norm>>(), METH_FASTCALL, nullptr},
+    {"rms_norm", entry<ready<rms_norm>>(), METH_FASTCALL, nullptr},
+    {"quantize_fp8", entry<ready<quantize_fp8>>(), METH_FASTCALL, nullptr},
+    {"gemm_fp8", entry<ready<gemm_fp8>>(), METH_FASTCALL, nullptr},
     {"setup", entry<setup>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -430,6 +430,78 @@ SVDQ_API int svdq_layer_norm(const void* x, int64_t ldx, const void* weight, con
                               void* y, int64_t ldy, int M, int K, float eps, int dtype,
                               void* stream);
 
+/* ---------------------------------------------------------------------
+ * 8-bit operators of a block that is served in 8 bits.  Codes are OCP e4m3
+ * (largest value 448, no infinity), a byte each; arithmetic is fp32 between
+ * load and the one rounding at the end.  They allocate nothing; conventions,
+ * errors and streams are those of the hot calls.
+ *
+ * Matrices of codes are dense [rows][K], 16-byte aligned, K % 16 == 0, with a
+ * scale for each block of 128 values along K (the last may be shorter):
+ *   activations  scales fp32 [ceil(K / 128)][rows], group-major
+ *   weights      scales fp32 [ceil(N / 128)][ceil(K / 128)], one for
+ *                128 x 128 values
+ * Rule: s = max(amax, 2^-100) / 448, code = e4m3(fp32(v * fp32(1 / s))) to
+ * nearest even.  amax passes over NaN; a NaN's code is NaN; an infinity makes
+ * s infinite and the block's codes 0 and NaN, so that it is not lost.
+ * --------------------------------------------------------------------- */
+#define SVDQ_FP8_BLOCK 128
+
+/* Root-mean-square norm with the residual's addition:
+ *
+ *   h = x [+ residual],   y = h rstd [* weight],   rstd = 1 / sqrt(mean(h^2) + eps)
+ *
+ *   x         (dev) [M][K], row stride ldx
+ *   residual  (dev) [M][K], row stride ldr, or NULL
+ *   weight    (dev) [K], or NULL
+ *   sum       (dev) [M][K], row stride ld_sum, out: h rounded once, or NULL;
+ *             may be x or residual
+ *   y         (dev) [M][K], row stride ldy, out, or NULL; may be x or residual
+ *   yq, ys    (dev) codes and scales of y, out, or both NULL; taken from the
+ *             fp32 y (rounded once)
+ * Either y or yq and ys is given.  y is taken from h in fp32, not from its
+ * rounding.  The mean of squares is an fp32 sum: rows past about 2^60 in
+ * magnitude overflow it.  sum and y do not overlap.
+ * 1 <= M <= 2^31 - 2^16; K from 1 to 65536, K % 16 == 0 for codes; eps >= 0
+ * and finite.  16-bit pointers need 2-byte alignment only. */
+SVDQ_API int svdq_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                              void* sum, int64_t ld_sum, void* y, int64_t ldy, uint8_t* yq, float* ys,
+                              int M, int K, float eps, int dtype, void* stream);
+
+/* Codes and scales of activations x (dev) [M][K], row stride ldx, bf16 or
+ * fp16: xq (dev) [M][K], xs (dev) [ceil(K / 128)][M], out.
+ * 1 <= M <= 2^31 - 2^16; K a multiple of 16 to 2^22. */
+SVDQ_API int svdq_quantize_fp8(const void* x, int64_t ldx, uint8_t* xq, float* xs, int M, int K, int dtype,
+                              void* stream);
+
+/* Offline pack of a weight, on the CPU (all pointers host): w [N][K] bf16 or
+ * fp16 bits -> wq [N][K] codes, ws [ceil(N / 128)][ceil(K / 128)]. */
+SVDQ_API int svdq_pack_fp8(const uint16_t* w, int K, int N, int dtype, uint8_t* wq, float* ws);
+
+/* 8-bit linear with the epilogue of svdq_linear16:
+ *
+ *   z[m][n] = sum_g xs[g][m] ws[n / 128][g] sum_(k in block g) xq[m][k] wq[n][k]
+ *   y = residual + gate_r * act(z + bias),   r = row / group_rows
+ *
+ * xq, xs, wq, ws (dev) as above, xs and ws 4-byte aligned; bias, gate,
+ * residual, y, activation and dtype (theirs) as for svdq_linear16.  Sums are
+ * fp32, the blocks' in their order, but that the matrix core takes the 8-bit
+ * products of 8 consecutive k to the largest one's exponent E and cuts what
+ * lies below 2^(E - 13) (about 1e-4 of a result of 4096 products); y is
+ * rounded once and overlaps no operand but residual.
+ * M, N >= 1, M at most 2^31 - 2^16, N at most 2^28 - 32, fewer than 2^24 tiles
+ * of 64 x 64 in the result; K a multiple of 16 to 2^22.
+ * workspace (dev, 16-byte aligned): with the bytes that
+ * svdq_gemm_fp8_workspace_size names, grids that would leave the device idle
+ * are cut along K into fp32 parts that a second kernel adds in a fixed order;
+ * with NULL or fewer bytes they run in one piece.  Results are
+ * deterministic. */
+SVDQ_API int svdq_gemm_fp8_workspace_size(int M, int N, int K, size_t* out_bytes);
+SVDQ_API int svdq_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const void* bias,
+                              const void* gate, int64_t ld_gate, int group_rows, const void* residual, int64_t ldr,
+                              void* y, int64_t ldy, int M, int N, int K, int activation, int dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* Measurement hook: the dense matrix-core rate this GPU sustains.  Each of
  * `blocks` workgroups (4 waves; launch two per CU) issues 8 * iters
  * independent v_mfma_scale_f32_32x32x64_f8f6f4 per wave, with FP8 operands
@@ -455,17 +527,19 @@ SVDQ_API int svdq_debug_group_partials(const uint8_t* xq, const uint8_t* wq,
                               int m0, int n0, int mt, int nt,
                               int32_t* out, void* stream);
 
-/* Test hooks (host): the schedule that svdq_attention and svdq_linear16 take
- * for these sizes, given the workspace that they name for them.
+/* Test hooks (host): the schedule that svdq_attention, svdq_linear16 and
+ * svdq_gemm_fp8 take for these sizes, given the workspace that they name for them.
  *   attention: plan[0] rows of a tile, [1] parts of its keys within a
  *   workgroup, [2] splits of them over workgroups, [3] workgroups that take
  *   equal shares of all keys (0: a tile's keys are one workgroup's)
  *   linear16: plan[0] rows and [1] channels of a tile, [2] waves of a
  *   workgroup, [3] splits along K; aligned != 0: rows of x and w are 16-byte
- *   aligned, which takes K % 8 == 0 */
+ *   aligned, which takes K % 8 == 0
+ *   gemm_fp8: as for linear16 */
 SVDQ_API int svdq_debug_attention_plan(int total_q, int total_k, int batch, int heads_q,
                               int heads_k, int head_dim, int causal, int32_t* plan);
 SVDQ_API int svdq_debug_linear16_plan(int M, int N, int K, int aligned, int32_t* plan);
+SVDQ_API int svdq_debug_gemm_fp8_plan(int M, int N, int K, int32_t* plan);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,120 @@
+"""The 8-bit operators on the host: their C entry points refuse bad arguments
+before anything is launched, and the weight's pack follows its rule."""
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+import bit_quantized_diffusion_amd as bq
+from tests._reference8 import pack_plain
+
+FAKE = ctypes.c_void_p(0x10000)      # aligned, never dereferenced (validation fails first)
+OFF = ctypes.c_void_p(0x10008)       # 8-byte aligned
+ODD = ctypes.c_void_p(0x10001)
+BAD, SHAPE = bq.SVDQ_ERR_INVALID_ARG, bq.SVDQ_ERR_SHAPE
+
+
+def _gpu_present():
+    return torch.cuda.is_available()
+
+
+NORM = dict(x=FAKE, ldx=64, residual=FAKE, ldr=64, weight=FAKE, sum=FAKE, ld_sum=64, y=FAKE, ldy=64, yq=None, ys=None, m=8, k=64,
+            eps=1e-6, dtype=0)
+CODES = dict(NORM, y=None, yq=FAKE, ys=FAKE)
+QUANT = dict(x=FAKE, ldx=64, xq=FAKE, xs=FAKE, m=8, k=64, dtype=0)
+GEMM = dict(xq=FAKE, xs=FAKE, wq=FAKE, ws=FAKE, bias=FAKE, gate=FAKE, ld_gate=32, rows=4, residual=FAKE, ldr=32, y=FAKE, ldy=32, m=8,
+            n=32, k=64, act=0, dtype=0, ws_=None, size=0)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), BAD), (dict(y=None), BAD), (dict(yq=FAKE, ys=FAKE), BAD), (dict(x=ODD), BAD), (dict(residual=ODD), BAD), (dict(sum=ODD), BAD),
+    (dict(eps=-1.0), BAD), (dict(eps=math.nan), BAD), (dict(eps=math.inf), BAD), (dict(dtype=2), BAD), (dict(m=0), SHAPE), (dict(k=0), SHAPE),
+    (dict(m=2 ** 31 - 100), SHAPE), (dict(k=65537, ldx=65537, ldr=65537, ld_sum=65537, ldy=65537), SHAPE), (dict(ldx=63), SHAPE),
+    (dict(ldr=63), SHAPE), (dict(ld_sum=63), SHAPE), (dict(ldy=63), SHAPE),
+])
+def test_rms_norm_refuses(kw, want):
+    assert bq.lib.svdq_rms_norm(*dict(NORM, **kw).values(), None) == want
+
+
+@pytest.mark.parametrize("kw,want", [(dict(ys=None), BAD), (dict(yq=None), BAD), (dict(yq=OFF), BAD), (dict(ys=ODD), BAD), (dict(k=40), SHAPE)])
+def test_rms_norm_codes_refuses(kw, want):
+    assert bq.lib.svdq_rms_norm(*dict(CODES, **kw).values(), None) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), BAD), (dict(xq=None), BAD), (dict(xs=None), BAD), (dict(x=ODD), BAD), (dict(xq=OFF), BAD), (dict(xs=ODD), BAD), (dict(dtype=9), BAD),
+    (dict(m=0), SHAPE), (dict(k=0), SHAPE), (dict(k=8), SHAPE), (dict(k=72), SHAPE), (dict(ldx=63), SHAPE), (dict(k=(1 << 22) + 16, ldx=1 << 23), SHAPE),
+])
+def test_quantize_refuses(kw, want):
+    assert bq.lib.svdq_quantize_fp8(*dict(QUANT, **kw).values(), None) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(xq=None), BAD), (dict(xs=None), BAD), (dict(wq=None), BAD), (dict(ws=None), BAD), (dict(y=None), BAD), (dict(xq=OFF), BAD),
+    (dict(wq=OFF), BAD), (dict(xs=ODD), BAD), (dict(ws=ODD), BAD), (dict(y=ODD), BAD), (dict(residual=ODD), BAD), (dict(ws_=OFF), BAD),
+    (dict(act=3), BAD), (dict(dtype=-1), BAD), (dict(m=0), SHAPE), (dict(n=0), SHAPE), (dict(k=0), SHAPE), (dict(k=72), SHAPE),
+    (dict(k=(1 << 22) + 16), SHAPE), (dict(ldy=31), SHAPE), (dict(ldr=31), SHAPE), (dict(ld_gate=31), SHAPE), (dict(rows=0), SHAPE),
+    (dict(m=2 ** 31 - 100), SHAPE), (dict(n=2 ** 28, ldy=2 ** 28, ldr=2 ** 28, ld_gate=2 ** 28), SHAPE),
+    (dict(m=2 ** 29, n=128, ldy=128, ldr=128, ld_gate=128), SHAPE),
+])
+def test_gemm_refuses(kw, want):
+    assert bq.lib.svdq_gemm_fp8(*dict(GEMM, **kw).values(), None) == want
+
+
+def test_workspace_and_plan():
+    out, plan = ctypes.c_size_t(7), (ctypes.c_int32 * 4)()
+    assert bq.lib.svdq_gemm_fp8_workspace_size(1, 1, 16, None) == BAD and bq.lib.svdq_debug_gemm_fp8_plan(1, 1, 16, None) == BAD
+    assert bq.lib.svdq_gemm_fp8_workspace_size(1, 1, 24, ctypes.byref(out)) == SHAPE and out.value == 0
+    assert bq.lib.svdq_debug_gemm_fp8_plan(0, 1, 16, plan) == SHAPE
+    assert bq.gemm_fp8_workspace_size(4608, 12288, 4096) == 0 and bq.gemm_fp8_workspace_size(8, 64, 4096) == 0
+    assert bq.gemm_fp8_workspace_size(100, 256, 8192) % (100 * 256 * 4) == 0
+
+
+@pytest.mark.skipif(_gpu_present(), reason="checks the no-device path")
+def test_no_device():
+    for call in (lambda: bq.lib.svdq_rms_norm(*NORM.values(), None), lambda: bq.lib.svdq_rms_norm(*CODES.values(), None),
+                 lambda: bq.lib.svdq_quantize_fp8(*QUANT.values(), None), lambda: bq.lib.svdq_gemm_fp8(*GEMM.values(), None)):
+        assert call() == bq.SVDQ_ERR_UNSUPPORTED_DEVICE
+
+
+def test_host_tensors_are_refused():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    w, s = torch.zeros(16, 64, dtype=torch.uint8).view(torch.float8_e4m3fn), torch.zeros(1, 1)
+    for call in (lambda: bq.rms_norm(x), lambda: bq.rms_norm_fp8(x), lambda: bq.quantize_fp8(x), lambda: bq.linear_fp8(x, w, s),
+                 lambda: bq.gemm_fp8(w, s, w, s), lambda: bq.rms_norm([1.0]), lambda: bq.gemm_fp8(None, s, w, s)):
+        with pytest.raises(TypeError):
+            call()
+
+
+@pytest.mark.parametrize("n,k", [(1, 16), (128, 128), (130, 272), (300, 1040)])
+def test_pack(n, k):
+    g = torch.Generator().manual_seed(n)
+    for dtype in (torch.bfloat16, torch.float16):
+        w = (torch.randn(n, k, generator=g) * torch.exp(torch.randn(n, k, generator=g) * 2)).to(dtype)
+        w[0, :3] = torch.tensor([0.0, -0.0, 5.0]).to(dtype)
+        q, s = bq.pack_fp8(w)
+        want_q, want_s = pack_plain(w)
+        assert torch.equal(s, want_s)
+        assert torch.equal(q.view(torch.uint8), want_q.view(torch.uint8))
+
+
+def test_pack_of_every_step():
+    """Values that meet every code, and the middle between two of them."""
+    codes = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    w = torch.cat([codes, (codes[1:] + codes[:-1]) / 2, -codes, torch.tensor([448.0])])
+    w = torch.nn.functional.pad(w, (0, 512 - w.numel())).view(4, 128).to(torch.bfloat16)   # the largest, 448: scale 1
+    assert w.float().abs().max() == 448
+    q, s = bq.pack_fp8(w)
+    assert (s == 1).all()
+    assert torch.equal(q.view(torch.uint8), w.float().to(torch.float8_e4m3fn).view(torch.uint8))
+
+
+def test_pack_refuses():
+    for w in (torch.zeros(4, 16), torch.zeros(4, dtype=torch.bfloat16), None):
+        with pytest.raises(TypeError):
+            bq.pack_fp8(w)
+    for w in (torch.zeros(4, 24, dtype=torch.bfloat16), torch.zeros(0, 16, dtype=torch.float16)):
+        with pytest.raises(bq.SvdqError):
+            bq.pack_fp8(w)
