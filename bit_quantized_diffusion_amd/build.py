@@ -41,7 +41,7 @@ HOST_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-pthread",
               "-Wall", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", f"-I{ROCM}/include"]
 
 KERNEL_SOURCES = ["svdq_kernels.hip", "svdq_attention.hip", "svdq_linear16.hip", "svdq_norm.hip",
-                  "svdq_linear8.hip"]
+                  "svdq_linear8.hip", "svdq_cache.hip", "svdq_attention8.hip"]
 HOST_SOURCES = ["svdq_abi.cpp", "svdq_pack.cpp"]
 PYTHON_SOURCE = "svdq_python.cpp"
 

@@ -86,6 +86,25 @@ int check_gemm_fp8_shape(int M, int N, int K) {
   return check_codes(K);
 }
 
+int check_paged_shape(int total, int batch, int width, int heads_q, int heads_k, int head_dim) {
+  if (total < 0 || batch < 1 || width < 1 || heads_q < 1 || heads_k < 1 || heads_q % heads_k) return SVDQ_ERR_SHAPE;
+  if (head_dim < 16 || head_dim > 128 || head_dim % 16) return SVDQ_ERR_SHAPE;
+  // pages of all tiles of 16 rows are counted in 31 bits; a launch holds less
+  // than 2^32 threads: 256 for such a tile, for a touched page of a head, or
+  // for a token's queries
+  const long long rows = static_cast<long long>(total) * (heads_q / heads_k), hk = heads_k;
+  if (rows > kMostRows || rows / 16 + 2LL * batch + total >= (1LL << 24) / hk) return SVDQ_ERR_SHAPE;
+  if ((rows / 16 + batch) * hk >= (1LL << 31) / width) return SVDQ_ERR_SHAPE;
+  return SVDQ_OK;
+}
+
+// strides in elements: not negative, far from overflow
+bool strides_fit(const int64_t* strides, int n, int multiple) {
+  for (int i = 0; i < n; ++i)
+    if (strides[i] < 0 || strides[i] % multiple || strides[i] > 1LL << 40) return false;
+  return true;
+}
+
 int hip_status(int e) { return e == 0 ? SVDQ_OK : SVDQ_ERR_HIP; }
 
 }  // namespace
@@ -482,6 +501,62 @@ int svdq_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const f
                                          y, ldy, M, N, K, activation, dtype, workspace, workspace_bytes, stream));
 }
 
+int svdq_cache_append(const void* q, const void* k, const void* v, void* q_out, const int64_t* strides, uint8_t* k_cache,
+                      uint8_t* v_cache, int8_t* exponents, int pages, const int32_t* block_table, int table_width,
+                      const int32_t* lengths, const int32_t* cu_seqlens, int batch, int total, int heads_q, int heads_k,
+                      int head_dim, const float* rope, int rope_rows, int rotary, int interleaved, int dtype, void* stream) {
+  int st = check_dtype(dtype);
+  if (st) return st;
+  if ((st = check_paged_shape(total, batch, table_width, heads_q, heads_k, head_dim))) return st;
+  if (pages < 1 || (!cu_seqlens && total != batch)) return SVDQ_ERR_SHAPE;
+  if (rotary < 0 || rotary % 16 || rotary > head_dim || !rope != !rotary || (rope && rope_rows < 1)) return SVDQ_ERR_SHAPE;
+  if (!strides || !k_cache || !v_cache || !exponents || !block_table || !lengths || !q != !q_out ||
+      (total > 0 && (!k || !v)))
+    return SVDQ_ERR_INVALID_ARG;
+  if (!aligned2(q) || !aligned2(k) || !aligned2(v) || !aligned2(q_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned4(block_table) || !aligned4(lengths) || !aligned4(cu_seqlens) || !aligned4(rope))
+    return SVDQ_ERR_INVALID_ARG;
+  if (!strides_fit(strides, 8, 1)) return SVDQ_ERR_INVALID_ARG;
+  if ((st = current_device_ok())) return st;
+  if (total == 0) return SVDQ_OK;
+  return hip_status(svdq_launch_cache_append(q, k, v, q_out, strides, k_cache, v_cache, exponents, pages, block_table,
+                                             table_width, lengths, cu_seqlens, batch, total, heads_q, heads_k, head_dim, rope,
+                                             rope_rows, rotary, interleaved != 0, dtype, stream));
+}
+
+int svdq_attention_paged_workspace_size(int total, int batch, int table_width, int heads_q, int heads_k, int head_dim,
+                                        size_t* out_bytes) {
+  if (!out_bytes) return SVDQ_ERR_INVALID_ARG;
+  *out_bytes = 0;
+  const int st = check_paged_shape(total, batch, table_width, heads_q, heads_k, head_dim);
+  if (st) return st;
+  *out_bytes = svdq_attention_paged_plan_bytes(total, batch, table_width, heads_q, heads_k, head_dim);
+  return SVDQ_OK;
+}
+
+int svdq_attention_paged(const void* q, void* o, float* lse, const int64_t* strides, const uint8_t* k_cache,
+                         const uint8_t* v_cache, const int8_t* exponents, int pages, const int32_t* block_table,
+                         int table_width, const int32_t* lengths, const int32_t* cu_seqlens, int batch, int total,
+                         int heads_q, int heads_k, int head_dim, float scale, int causal, int dtype, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  int st = check_dtype(dtype);
+  if (st) return st;
+  if ((st = check_paged_shape(total, batch, table_width, heads_q, heads_k, head_dim))) return st;
+  if (pages < 1 || (!cu_seqlens && total != batch)) return SVDQ_ERR_SHAPE;
+  if (!strides || !k_cache || !v_cache || !exponents || !block_table || !lengths || (total > 0 && (!q || !o)))
+    return SVDQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(workspace) ||
+      !aligned4(lse) || !aligned4(block_table) || !aligned4(lengths) || !aligned4(cu_seqlens))
+    return SVDQ_ERR_INVALID_ARG;
+  if (!strides_fit(strides, 4, 8)) return SVDQ_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || std::isinf(scale * 2.f)) return SVDQ_ERR_INVALID_ARG;
+  if ((st = current_device_ok())) return st;
+  if (total == 0) return SVDQ_OK;
+  return hip_status(svdq_launch_attention_paged(q, o, lse, strides, k_cache, v_cache, exponents, pages, block_table,
+                                                table_width, lengths, cu_seqlens, batch, total, heads_q, heads_k, head_dim,
+                                                scale, causal != 0, dtype, workspace, workspace_bytes, stream));
+}
+
 int svdq_bench_mfma_ceiling(int precision, int blocks, int iters, float* out, void* stream) {
   if (!out || !aligned16(out)) return SVDQ_ERR_INVALID_ARG;
   if (precision != SVDQ_INT4 && precision != SVDQ_MXFP4) return SVDQ_ERR_INVALID_ARG;
@@ -520,6 +595,15 @@ int svdq_debug_linear16_plan(int M, int N, int K, int aligned, int32_t* plan) {
   if (st) return st;
   if (aligned && K % 8) return SVDQ_ERR_SHAPE;
   svdq_linear16_plan(M, N, K, aligned, plan);
+  return SVDQ_OK;
+}
+
+int svdq_debug_attention_paged_plan(int total, int batch, int table_width, int heads_q, int heads_k, int head_dim,
+                                    int32_t* plan) {
+  if (!plan) return SVDQ_ERR_INVALID_ARG;
+  const int st = check_paged_shape(total, batch, table_width, heads_q, heads_k, head_dim);
+  if (st) return st;
+  svdq_attention_paged_plan(total, batch, table_width, heads_q, heads_k, head_dim, plan);
   return SVDQ_OK;
 }
 

@@ -108,6 +108,18 @@ int svdq_launch_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, 
                          const void* gate, int64_t ld_gate, int group_rows, const void* residual, int64_t ldr, void* y,
                          int64_t ldy, int M, int N, int K, int activation, int dtype, void* workspace,
                          size_t workspace_bytes, void* stream);
+int svdq_launch_cache_append(const void* q, const void* k, const void* v, void* q_out, const int64_t* strides,
+                             uint8_t* k_cache, uint8_t* v_cache, int8_t* exponents, int pages, const int32_t* table,
+                             int width, const int32_t* lengths, const int32_t* cu, int batch, int total, int heads_q,
+                             int heads_k, int head_dim, const float* rope, int rope_rows, int rotary, int interleaved,
+                             int dtype, void* stream);
+size_t svdq_attention_paged_plan_bytes(int total, int batch, int width, int heads_q, int heads_k, int head_dim);
+void svdq_attention_paged_plan(int total, int batch, int width, int heads_q, int heads_k, int head_dim, int32_t* plan);
+int svdq_launch_attention_paged(const void* q, void* o, float* lse, const int64_t* strides, const uint8_t* k_cache,
+                                const uint8_t* v_cache, const int8_t* exponents, int pages, const int32_t* table, int width,
+                                const int32_t* lengths, const int32_t* cu, int batch, int total, int heads_q, int heads_k,
+                                int head_dim, float scale, int causal, int dtype, void* workspace, size_t workspace_bytes,
+                                void* stream);
 int svdq_launch_mfma_ceiling(int precision, int blocks, int iters, float* out, void* stream);
 int svdq_launch_unfused_linear_noalloc(const void* x, int M, int K, const float* smooth_inv, const void* lora_down,
                                        int rank, const uint8_t* wq, const void* ws, const void* lora_up,

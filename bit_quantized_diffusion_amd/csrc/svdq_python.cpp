@@ -47,7 +47,7 @@ class Ref {
   PyObject* p_;
 };
 
-constexpr int kDims = 3;
+constexpr int kDims = 5;
 
 // What a call needs to know of a tensor.  More than kDims dimensions: dims
 // alone is true.
@@ -131,7 +131,7 @@ bool same_kind(PyObject* o, const Tensor& first, const char* name, Tensor& t) {
 
 // Tensor t, read from o, has this shape and a dense last dimension.
 bool shaped(PyObject* o, const Tensor& t, int dims, int64_t a, int64_t b, int64_t c, const char* name) {
-  const int64_t want[kDims] = {a, b, c};
+  const int64_t want[3] = {a, b, c};
   bool same = t.dims == dims;
   for (int i = 0; same && i < dims; ++i) same = t.shape[i] == want[i];
   if (!same) {
@@ -231,7 +231,7 @@ PyObject* output(PyObject* given, PyObject* x, const Tensor& first, int dims, in
   }
   PyObject* o = dims == 2 ? new_empty(x, {a, b}) : new_empty(x, {a, b, c});
   if (!o) return nullptr;
-  const int64_t shape[kDims] = {a, b, c};
+  const int64_t shape[3] = {a, b, c};
   int64_t dense = 1;
   for (int i = dims - 1; i >= 0; --i) {
     t.shape[i] = shape[i];
@@ -669,6 +669,182 @@ PyObject* gemm_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return out.release();
 }
 
+// The paged cache (codes of keys and values, exponents) and where the
+// sequences of a call with `total` tokens stand in it.
+struct Paged {
+  Tensor k, v, exponents, table, lengths;
+  void* cu = nullptr;
+  int64_t batch = 0;
+
+  // args: k codes, v codes, exponents, block_table, lengths, cu_seqlens
+  bool init(PyObject* const* args, long device, int64_t total) {
+    if (!read(args[0], k) || k.dims != 4) return no_tensor("cache.k", "[pages][heads][64][head_dim]");
+    const int64_t pages = k.shape[0], heads = k.shape[1], D = k.shape[3];
+    if (!whole(args[0], k, g_f8, device, {pages, heads, SVDQ_PAGE, D}, "cache.k") ||
+        !read(args[1], v) || !whole(args[1], v, g_f8, device, {pages, heads, 4, D, 16}, "cache.v") ||
+        !read(args[2], exponents) || !whole(args[2], exponents, g_i8, device, {pages, heads, 2}, "cache.exponents"))
+      return named();
+    if (!read(args[4], lengths) || lengths.dims != 1) return no_tensor("lengths", "[batch]");
+    batch = lengths.shape[0];
+    if (!whole(args[4], lengths, g_i32, device, {batch}, "lengths")) return false;
+    if (!read(args[3], table) || table.dims != 2) return no_tensor("block_table", "[batch][width]");
+    if (!whole(args[3], table, g_i32, device, {batch, table.shape[1]}, "block_table")) return false;
+    if (args[5] == Py_None) {
+      if (total != batch) {
+        PyErr_Format(PyExc_ValueError, "without cu_seqlens each of the %lld sequences has one token, got %lld",
+                     static_cast<long long>(batch), static_cast<long long>(total));
+        return false;
+      }
+    } else {
+      Tensor first;
+      first.device = device;
+      int64_t n;
+      if (!starts(args[5], first, "cu_seqlens", cu, n)) return false;
+      if (n != batch) {
+        PyErr_SetString(PyExc_ValueError, "cu_seqlens: expected one entry more than lengths has");
+        return false;
+      }
+    }
+    return countable({pages, heads, D, batch, table.shape[1], total}, "cache");
+  }
+
+ private:
+  // an error is set, if not by read()
+  static bool named() { return PyErr_Occurred() ? false : no_tensor("cache", ""); }
+
+  static bool whole(PyObject*, const Tensor& t, PyObject* dtype, long device, std::initializer_list<int64_t> shape,
+                    const char* name) {
+    if (t.dtype != dtype || t.device != device) {
+      PyErr_Format(PyExc_TypeError, "%s: expected %S on cuda:%ld, got %S on device %ld", name, dtype, device, t.dtype, t.device);
+      return false;
+    }
+    bool fits = t.dims == static_cast<int>(shape.size());
+    int64_t dense = 1;
+    for (int i = t.dims - 1; fits && i >= 0; --i) {
+      fits = t.shape[i] == shape.begin()[i] && (t.shape[i] <= 1 || t.stride[i] == dense);
+      dense *= t.shape[i];
+    }
+    if (!fits) PyErr_Format(PyExc_ValueError, "%s: wrong shape for this cache and batch, or not contiguous", name);
+    return fits;
+  }
+};
+
+// strides of a tensor [tokens][heads][head_dim]; a dimension of size 1 has that of a dense one
+void strides_of(const Tensor& t, int64_t* to) {
+  to[0] = t.shape[0] > 1 ? t.stride[0] : t.shape[1] * t.shape[2];
+  to[1] = t.shape[1] > 1 ? t.stride[1] : t.shape[2];
+}
+
+// cache_append(k codes, v codes, exponents, block_table, lengths, cu_seqlens, k, v, q, rope, interleaved, q_out)
+PyObject* cache_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!count_of("cache_append", n, 12)) return nullptr;
+  Tensor k, v, q, out, rope;
+  int code;
+  if (!operand(args[6], 3, "k", "[tokens][heads][head_dim]", k, code)) return nullptr;
+  const int64_t total = k.shape[0], heads_k = k.shape[1], D = k.shape[2];
+  if (!like(args[7], k, 3, total, heads_k, D, "v", v)) return nullptr;
+  Paged p;
+  if (!p.init(args, k.device, total)) return nullptr;
+  if (p.k.shape[1] != heads_k || p.k.shape[3] != D) {
+    PyErr_Format(PyExc_ValueError, "k: the cache has %lld heads of %lld", static_cast<long long>(p.k.shape[1]),
+                 static_cast<long long>(p.k.shape[3]));
+    return nullptr;
+  }
+  int64_t rotary = 0, rope_rows = 0;
+  if (args[9] != Py_None) {
+    if (!read(args[9], rope) || rope.dims != 2) {
+      no_tensor("rope", "[positions][rotary]");
+      return nullptr;
+    }
+    rope_rows = rope.shape[0];
+    rotary = rope.shape[1];
+    if (!exactly(args[9], g_f32, k.device, 2, rope_rows, rotary, 0, "rope", rope)) return nullptr;
+  }
+  const int interleaved = PyObject_IsTrue(args[10]);
+  if (interleaved < 0) return nullptr;
+  Ref rotated;
+  int64_t heads_q = heads_k, strides[8] = {};
+  if (args[8] != Py_None) {
+    if (!same_kind(args[8], k, "q", q)) return nullptr;
+    heads_q = q.dims == 3 ? q.shape[1] : 0;
+    if (!shaped(args[8], q, 3, total, heads_q, D, "q")) return nullptr;
+    rotated.reset(output(args[11], args[8], k, 3, total, heads_q, D, out));
+    if (!rotated) return nullptr;
+    strides_of(q, strides);
+    strides_of(out, strides + 6);
+  } else if (args[11] != Py_None) {
+    PyErr_SetString(PyExc_ValueError, "q_out without q");
+    return nullptr;
+  }
+  if (!countable({heads_q, rope_rows, rotary}, "cache_append")) return nullptr;
+  strides_of(k, strides + 2);
+  strides_of(v, strides + 4);
+  if (!run(k.device, [&](void* stream) {
+        return svdq_cache_append(q.ptr, k.ptr, v.ptr, out.ptr, strides, static_cast<uint8_t*>(p.k.ptr),
+                                 static_cast<uint8_t*>(p.v.ptr), static_cast<int8_t*>(p.exponents.ptr),
+                                 static_cast<int>(p.k.shape[0]), static_cast<int32_t*>(p.table.ptr),
+                                 static_cast<int>(p.table.shape[1]), static_cast<int32_t*>(p.lengths.ptr),
+                                 static_cast<int32_t*>(p.cu), static_cast<int>(p.batch), static_cast<int>(total),
+                                 static_cast<int>(heads_q), static_cast<int>(heads_k), static_cast<int>(D),
+                                 static_cast<float*>(rope.ptr), static_cast<int>(rope_rows), static_cast<int>(rotary),
+                                 interleaved, code, stream);
+      }))
+    return nullptr;
+  if (rotated) return rotated.release();
+  Py_RETURN_NONE;
+}
+
+// attention_paged(k codes, v codes, exponents, block_table, lengths, cu_seqlens, q, causal, scale, out, return_lse,
+// workspace)
+PyObject* attention_paged(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!count_of("attention_paged", n, 12)) return nullptr;
+  Tensor q, o, l;
+  int code;
+  if (!operand(args[6], 3, "q", "[tokens][heads][head_dim]", q, code)) return nullptr;
+  const int64_t total = q.shape[0], heads_q = q.shape[1], D = q.shape[2];
+  Paged p;
+  if (!p.init(args, q.device, total)) return nullptr;
+  const int64_t heads_k = p.k.shape[1];
+  if (p.k.shape[3] != D) {
+    PyErr_Format(PyExc_ValueError, "q: the cache has heads of %lld", static_cast<long long>(p.k.shape[3]));
+    return nullptr;
+  }
+  if (!countable({heads_q}, "attention_paged")) return nullptr;
+  const int causal = PyObject_IsTrue(args[7]), with_lse = PyObject_IsTrue(args[10]);
+  if (causal < 0 || with_lse < 0) return nullptr;
+  double scale = D > 1 ? 1.0 / sqrt(static_cast<double>(D)) : 1.0;
+  if (args[8] != Py_None) {
+    scale = PyFloat_AsDouble(args[8]);
+    if (scale == -1.0 && PyErr_Occurred()) return nullptr;
+  }
+  Ref out(output(args[9], args[6], q, 3, total, heads_q, D, o)), lse;
+  if (!out) return nullptr;
+  if (with_lse) {
+    lse.reset(new_empty(args[6], {total, heads_q}, g_f32));
+    if (!lse) return nullptr;
+    l.ptr = pointer_of(lse.get());
+  }
+  int64_t strides[4];
+  strides_of(q, strides);
+  strides_of(o, strides + 2);
+  const int t = static_cast<int>(total), b = static_cast<int>(p.batch), w = static_cast<int>(p.table.shape[1]);
+  const int hq = static_cast<int>(heads_q), hk = static_cast<int>(heads_k), d = static_cast<int>(D);
+  size_t bytes = 0, size;
+  if (args[11] != Py_None && !fine(svdq_attention_paged_workspace_size(t, b, w, hq, hk, d, &bytes))) return nullptr;
+  void* ws;
+  Ref keep;
+  if (!workspace_of(args[11], args[6], q, bytes, ws, size, keep)) return nullptr;
+  if (!run(q.device, [&](void* stream) {
+        return svdq_attention_paged(q.ptr, o.ptr, static_cast<float*>(l.ptr), strides, static_cast<uint8_t*>(p.k.ptr),
+                                    static_cast<uint8_t*>(p.v.ptr), static_cast<int8_t*>(p.exponents.ptr),
+                                    static_cast<int>(p.k.shape[0]), static_cast<int32_t*>(p.table.ptr), w,
+                                    static_cast<int32_t*>(p.lengths.ptr), static_cast<int32_t*>(p.cu), b, t, hq, hk, d,
+                                    static_cast<float>(scale), causal, code, ws, size, stream);
+      }))
+    return nullptr;
+  return with_lse ? PyTuple_Pack(2, out.get(), lse.get()) : out.release();
+}
+
 // setup(Tensor, bfloat16, float16, float32, uint8, int32, current stream, current device, set device, check, e4m3, int8)
 PyObject* setup(PyObject*, PyObject* const* args, Py_ssize_t n) {
   PyObject** const to[] = {&g_tensor, &g_bf16, &g_f16, &g_f32, &g_u8, &g_i32, &g_stream, &g_current, &g_set_device, &g_check, &g_f8, &g_i8};
@@ -706,6 +882,8 @@ PyMethodDef g_methods[] = {
     {"rms_norm", entry<ready<rms_norm>>(), METH_FASTCALL, nullptr},
     {"quantize_fp8", entry<ready<quantize_fp8>>(), METH_FASTCALL, nullptr},
     {"gemm_fp8", entry<ready<gemm_fp8>>(), METH_FASTCALL, nullptr},
+    {"cache_append", entry<ready<cache_append>>(), METH_FASTCALL, nullptr},
+    {"attention_paged", entry<ready<attention_paged>>(), METH_FASTCALL, nullptr},
     {"setup", entry<setup>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -502,6 +502,87 @@ SVDQ_API int svdq_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq
                               void* y, int64_t ldy, int M, int N, int K, int activation, int dtype, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/* Keys and values of packed sequences in a paged cache of 8-bit codes.
+ *
+ *   k_cache     (dev) [pages][heads_k][64][head_dim] codes, by place
+ *   v_cache     (dev) [pages][heads_k][4][head_dim][16] codes: place p of the
+ *               page at [p / 4 % 4][d][4 (p / 16) + p % 4]
+ *   exponents   (dev) [pages][heads_k][2] int8: value = code * 2^e, of keys
+ *               and of values; taken as cut to [-40, 40]
+ *   block_table (dev) [batch][table_width] int32: the page of positions 64 i
+ *               to 64 i + 63 of each sequence
+ *   lengths     (dev) [batch] int32: tokens of each sequence in the cache, the
+ *               new ones (of this call's q, k and v) included
+ *   cu_seqlens  (dev) [batch+1] int32: sequence b has tokens cu[b] .. cu[b+1]-1
+ *               of the pack, the last of its positions; NULL: one token each
+ *               (batch == total)
+ * Entries of the table that name no page (below 0, or pages and more) have
+ * none: nothing is written there, and their keys are hidden.  Positions past
+ * the table, and tokens before position 0, are passed over in the same way.
+ * Whatever these arrays hold, no access leaves the tensors.
+ *
+ * svdq_cache_append writes the new tokens' keys and values, and rotates q:
+ *
+ *   q         (dev) [total][heads_q][head_dim] and q_out, its rotation; or both
+ *             NULL.  q_out may be q itself (with its strides) and overlaps
+ *             nothing else.
+ *   k, v      (dev) [total][heads_k][head_dim]
+ *   rope      (dev) fp32 [rope_rows][rotary]: rotary / 2 cosines and as many
+ *             sines for each position (those past the last row take it); or
+ *             NULL with rotary == 0: nothing is rotated
+ *   strides   (host) 8 strides in elements: q token, q head, k token, k head,
+ *             v token, v head, q_out token, q_out head; not negative, the last
+ *             dimension is dense, 2-byte alignment suffices
+ * Of the first `rotary` values of a head (a multiple of 16, at most head_dim)
+ * the pairs are i and i + rotary / 2, or (interleaved != 0) 2 i and 2 i + 1:
+ * (a, b) -> (a cos - b sin, b cos + a sin).  q is rounded once to its type, k
+ * and v once to their codes.  A page's exponent (of each head, keys and values
+ * apart) is the least e with amax <= 448 * 2^e over the finite values that
+ * enter it, cut to [-40, 40], and not below the one it has if it holds earlier
+ * tokens of the sequence; those codes are then rescaled (rounded to nearest
+ * even, exact but for codes below 2^-6).  Values past 448 * 2^40 become that;
+ * what is not finite becomes NaN.  Other places of a page stay as they are.
+ * Tokens of no sequence are not appended, and their q is not rotated.  Two
+ * sequences may share pages that no call appends to; a page that is written
+ * for two places at once holds either's.
+ *
+ * svdq_attention_paged lets q's tokens attend to their sequences in the cache:
+ *
+ *   q, o      (dev) [total][heads_q][head_dim], 16-byte aligned
+ *   lse       (dev) [total][heads_q] fp32, out, or NULL: log sum_j exp(s_ij)
+ *   strides   (host) 4 strides in elements: q token, q head, o token, o head;
+ *             multiples of 8, not negative
+ * Query head h reads key head h / (heads_q / heads_k).  causal != 0: query i of
+ * n sees keys j <= i + length - n, else all of its sequence's.  A query that
+ * sees no key, or belongs to no sequence, gives o = 0 and lse = -inf.  Pages'
+ * places past a sequence's length may hold anything; a NaN at a key that only
+ * causal masking hides can reach a query.  The codes are taken exactly; P is
+ * rounded to 16 bits for the matrix core; softmax statistics and sums are
+ * fp32.  o overlaps no operand.  0 < scale < 2^127.
+ * workspace (dev, 16-byte aligned): with the bytes that
+ * svdq_attention_paged_workspace_size names, calls with few queries a sequence
+ * cut the keys into equal shares, which a second kernel joins in a fixed
+ * order; with NULL or fewer bytes a workgroup runs through all keys of its
+ * queries.  Results are deterministic; the schedule goes by sizes alone.
+ *
+ * Both: head_dim a multiple of 16 from 16 to 128; heads_q a multiple of
+ * heads_k; batch, pages, table_width >= 1; total >= 0; caches 16-byte
+ * aligned; (total (heads_q / heads_k) / 16 + batch) heads_k table_width below
+ * 2^31, and (total (heads_q / heads_k) / 16 + 2 batch + total) heads_k below 2^24. */
+#define SVDQ_PAGE 64
+SVDQ_API int svdq_cache_append(const void* q, const void* k, const void* v, void* q_out, const int64_t* strides,
+                              uint8_t* k_cache, uint8_t* v_cache, int8_t* exponents, int pages,
+                              const int32_t* block_table, int table_width, const int32_t* lengths,
+                              const int32_t* cu_seqlens, int batch, int total, int heads_q, int heads_k, int head_dim,
+                              const float* rope, int rope_rows, int rotary, int interleaved, int dtype, void* stream);
+SVDQ_API int svdq_attention_paged_workspace_size(int total, int batch, int table_width, int heads_q, int heads_k,
+                              int head_dim, size_t* out_bytes);
+SVDQ_API int svdq_attention_paged(const void* q, void* o, float* lse, const int64_t* strides, const uint8_t* k_cache,
+                              const uint8_t* v_cache, const int8_t* exponents, int pages, const int32_t* block_table,
+                              int table_width, const int32_t* lengths, const int32_t* cu_seqlens, int batch, int total,
+                              int heads_q, int heads_k, int head_dim, float scale, int causal, int dtype,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
 /* Measurement hook: the dense matrix-core rate this GPU sustains.  Each of
  * `blocks` workgroups (4 waves; launch two per CU) issues 8 * iters
  * independent v_mfma_scale_f32_32x32x64_f8f6f4 per wave, with FP8 operands
@@ -527,19 +608,22 @@ SVDQ_API int svdq_debug_group_partials(const uint8_t* xq, const uint8_t* wq,
                               int m0, int n0, int mt, int nt,
                               int32_t* out, void* stream);
 
-/* Test hooks (host): the schedule that svdq_attention, svdq_linear16 and
- * svdq_gemm_fp8 take for these sizes, given the workspace that they name for them.
+/* Test hooks (host): the schedule that these operators take for these sizes, given the workspace that they name for them.
  *   attention: plan[0] rows of a tile, [1] parts of its keys within a
  *   workgroup, [2] splits of them over workgroups, [3] workgroups that take
  *   equal shares of all keys (0: a tile's keys are one workgroup's)
  *   linear16: plan[0] rows and [1] channels of a tile, [2] waves of a
  *   workgroup, [3] splits along K; aligned != 0: rows of x and w are 16-byte
  *   aligned, which takes K % 8 == 0
- *   gemm_fp8: as for linear16 */
+ *   gemm_fp8: as for linear16
+ *   attention_paged: plan[0] rows of a tile, [1] workgroups that take equal
+ *   shares of all keys (0: a tile's keys are one workgroup's) */
 SVDQ_API int svdq_debug_attention_plan(int total_q, int total_k, int batch, int heads_q,
                               int heads_k, int head_dim, int causal, int32_t* plan);
 SVDQ_API int svdq_debug_linear16_plan(int M, int N, int K, int aligned, int32_t* plan);
 SVDQ_API int svdq_debug_gemm_fp8_plan(int M, int N, int K, int32_t* plan);
+SVDQ_API int svdq_debug_attention_paged_plan(int total, int batch, int table_width, int heads_q, int heads_k,
+                              int head_dim, int32_t* plan);
 
 #ifdef __cplusplus
 }

@@ -118,3 +118,81 @@ def test_pack_refuses():
     for w in (torch.zeros(4, 24, dtype=torch.bfloat16), torch.zeros(0, 16, dtype=torch.float16)):
         with pytest.raises(bq.SvdqError):
             bq.pack_fp8(w)
+
+
+APPEND = dict(q=FAKE, k=FAKE, v=FAKE, q_out=FAKE, strides=(256, 64, 128, 64, 128, 64, 256, 64), k8=FAKE, v8=FAKE, e=FAKE, pages=4, table=FAKE,
+              width=2, lengths=FAKE, cu=FAKE, batch=2, total=10, hq=4, hk=2, d=64, rope=FAKE, rows=128, rotary=64, interleaved=0, dtype=0)
+PAGED = dict(q=FAKE, o=FAKE, lse=FAKE, strides=(256, 64, 256, 64), k8=FAKE, v8=FAKE, e=FAKE, pages=4, table=FAKE, width=2, lengths=FAKE, cu=FAKE,
+             batch=2, total=10, hq=4, hk=2, d=64, scale=0.125, causal=1, dtype=0, ws=None, n=0)
+
+
+def _call(fn, defaults, kw):
+    a = dict(defaults, **kw)
+    a["strides"] = None if a["strides"] is None else (ctypes.c_int64 * len(a["strides"]))(*a["strides"])
+    return fn(*a.values(), None)
+
+
+SHAPES = [
+    (dict(batch=0), SHAPE), (dict(total=-1), SHAPE), (dict(width=0), SHAPE), (dict(hq=0), SHAPE), (dict(hk=0), SHAPE), (dict(hk=3), SHAPE),
+    (dict(pages=0), SHAPE), (dict(d=8), SHAPE), (dict(d=72), SHAPE), (dict(d=144), SHAPE), (dict(cu=None), SHAPE), (dict(total=2 ** 24), SHAPE),
+    (dict(batch=2 ** 23), SHAPE), (dict(width=2 ** 30), SHAPE), (dict(total=2 ** 23, hq=512), SHAPE),
+    (dict(k8=None), BAD), (dict(v8=None), BAD), (dict(e=None), BAD), (dict(table=None), BAD), (dict(lengths=None), BAD), (dict(strides=None), BAD),
+    (dict(k8=OFF), BAD), (dict(v8=OFF), BAD), (dict(table=ODD), BAD), (dict(lengths=ODD), BAD), (dict(cu=ODD), BAD), (dict(dtype=2), BAD),
+]
+
+
+@pytest.mark.parametrize("kw,want", SHAPES + [
+    (dict(q=None), BAD), (dict(q_out=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD), (dict(k=ODD), BAD), (dict(q_out=ODD), BAD), (dict(rope=ODD), BAD),
+    (dict(strides=(256, 64, -128, 64, 128, 64, 256, 64)), BAD), (dict(strides=(256, 64, 128, 64, 128, 64, 1 << 41, 64)), BAD),
+    (dict(rotary=0), SHAPE), (dict(rope=None), SHAPE), (dict(rotary=24), SHAPE), (dict(rotary=80), SHAPE), (dict(rotary=-16), SHAPE), (dict(rows=0), SHAPE),
+])
+def test_append_refuses(kw, want):
+    assert _call(bq.lib.svdq_cache_append, APPEND, kw) == want
+
+
+@pytest.mark.parametrize("kw,want", SHAPES + [
+    (dict(q=None), BAD), (dict(o=None), BAD), (dict(q=OFF), BAD), (dict(o=OFF), BAD), (dict(lse=ODD), BAD), (dict(ws=OFF), BAD), (dict(scale=0.0), BAD),
+    (dict(scale=math.nan), BAD), (dict(scale=3e38), BAD), (dict(strides=(256, 60, 256, 64)), BAD), (dict(strides=(256, 64, -256, 64)), BAD),
+])
+def test_attention_paged_refuses(kw, want):
+    assert _call(bq.lib.svdq_attention_paged, PAGED, kw) == want
+
+
+def test_paged_workspace_and_plan():
+    out, plan = ctypes.c_size_t(7), (ctypes.c_int32 * 2)()
+    f, g = bq.lib.svdq_attention_paged_workspace_size, bq.lib.svdq_debug_attention_paged_plan
+    assert f(1, 1, 1, 1, 1, 64, None) == BAD and g(1, 1, 1, 1, 1, 64, None) == BAD
+    assert f(1, 1, 1, 3, 2, 64, ctypes.byref(out)) == SHAPE and out.value == 0 and g(1, 0, 1, 1, 1, 64, plan) == SHAPE
+    assert bq.attention_paged_workspace_size(1, 1, 256, 8, 2, 128) > 0 and bq.attention_paged_workspace_size(1, 1, 4, 8, 2, 128) == 0
+
+
+@pytest.mark.skipif(_gpu_present(), reason="checks the no-device path")
+def test_no_device_cache():
+    assert _call(bq.lib.svdq_cache_append, APPEND, {}) == bq.SVDQ_ERR_UNSUPPORTED_DEVICE
+    assert _call(bq.lib.svdq_attention_paged, PAGED, {}) == bq.SVDQ_ERR_UNSUPPORTED_DEVICE
+
+
+def test_host_caches_are_refused():
+    cache = bq.KVCache.allocate(2, 2, 32, device="cpu")
+    k, n = torch.zeros(1, 2, 32, dtype=torch.bfloat16), torch.ones(1, dtype=torch.int32)
+    for call in (lambda: bq.cache_append(cache, k, k, n[None], n), lambda: bq.attention_paged(k, cache, n[None], n)):
+        with pytest.raises(TypeError):
+            call()
+
+
+def test_cache_layout_and_angles():
+    """What `read` takes from where svdq.h says the codes lie."""
+    cache = bq.KVCache.allocate(3, 2, 16, device="cpu")
+    k, v = cache.k.view(torch.uint8), cache.v.view(torch.uint8)
+    one, two = 0x38, 0x40      # 1.0 and 2.0
+    k[2, 1, 5, 7] = one
+    v[0, 0, 37 // 4 % 4, 3, 37 // 16 * 4 + 37 % 4] = two
+    cache.exponents[2, 1, 0], cache.exponents[0, 0, 1] = -3, 4
+    keys, values = cache.read(torch.tensor([2, 0], dtype=torch.int32), 110)
+    assert keys.shape == values.shape == (110, 2, 16)
+    assert keys[5, 1, 7] == 0.125 and keys.count_nonzero() == 1
+    assert values[64 + 37, 0, 3] == 32.0 and values.count_nonzero() == 1
+    table = bq.rope_table(1 << 17, 64, device="cpu")
+    p, i = 99999, 3
+    angle = p * 10000.0 ** (-2 * i / 64)
+    assert abs(float(table[p, i]) - math.cos(angle)) < 1e-7 and abs(float(table[p, 32 + i]) - math.sin(angle)) < 1e-7
