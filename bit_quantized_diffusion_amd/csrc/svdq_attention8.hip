@@ -79,8 +79,15 @@ __device__ __forceinline__ int visible(const PagedArgs& a, const Tile& t, int r)
   return a.causal ? max(0, min(t.length, t.length - t.tokens + row / a.group + 1)) : t.length;
 }
 
-// 16 RT rows against pages: DC chunks of 64 dimensions.
-template <typename E, int DC, int RT>
+// 16 RT rows against pages: DC chunks of 64 dimensions.  Codes that no other
+// workgroup reads bypass the caches' keeping (ONCE; 64 caches of 3000 to 5300
+// tokens 111 -> 99 us).
+template <bool ONCE>
+__device__ __forceinline__ v4u codes16(const uint8_t* p) {
+  const v4u* const v = reinterpret_cast<const v4u*>(p);
+  return ONCE ? __builtin_nontemporal_load(v) : *v;
+}
+template <typename E, int DC, int RT, bool ONCE>
 struct Rows {
   v4u q[RT][DC][2];
   v4u k[4][DC], v[4 * DC];    // a page's codes as they lie
@@ -123,7 +130,7 @@ struct Rows {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int c = 0; c < DC; ++c)
-        k[i][c] = 64 * c + 16 * g < D ? *reinterpret_cast<const v4u*>(p + i * 16 * D + 64 * c) : v4u{0, 0, 0, 0};
+        k[i][c] = 64 * c + 16 * g < D ? codes16<ONCE>(p + i * 16 * D + 64 * c) : v4u{0, 0, 0, 0};
     ek = a.exponents[slot * 2];
     ev = a.exponents[slot * 2 + 1];
   }
@@ -133,7 +140,7 @@ struct Rows {
     const uint8_t* const p = a.v_cache + slot * kPage * D + (g * D + l16) * 16;
 #pragma unroll
     for (int d = 0; d < 4 * DC; ++d)
-      v[d] = d * 16 < D ? *reinterpret_cast<const v4u*>(p + d * 256) : v4u{0, 0, 0, 0};
+      v[d] = d * 16 < D ? codes16<ONCE>(p + d * 256) : v4u{0, 0, 0, 0};
   }
 
   // Pages first, first + step, ... before last; up to key `all_see` every row
@@ -246,10 +253,11 @@ __device__ __forceinline__ void put(const PagedArgs& a, const Tile& t, int r, in
   const int row = t.row0 + r, token = row / a.group, head = t.h * a.group + row - token * a.group;
   store8(a.o + (t.start + token) * a.ldo + head * a.hdo + d, pack8<E>(f), 8);
 }
+__device__ __forceinline__ float logarithm(float m, float l) { return l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY; }
 __device__ __forceinline__ void put_lse(const PagedArgs& a, const Tile& t, int r, float m, float l) {
   if (!a.lse) return;
   const int row = t.row0 + r, token = row / a.group, head = t.h * a.group + row - token * a.group;
-  a.lse[static_cast<int64_t>(t.start + token) * a.heads_q + head] = l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY;
+  a.lse[static_cast<int64_t>(t.start + token) * a.heads_q + head] = logarithm(m, l);
 }
 
 // Queries of no sequence: zeros.
@@ -267,16 +275,18 @@ __device__ __forceinline__ void pad(const PagedArgs& a, int block, int blocks) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows a sequence.  All keys of all tiles of 16 RT rows lie on one line of
-// pages; with shares every workgroup takes an equal part of it, whole tiles or
-// pieces, whose parts a second kernel joins; without, one workgroup takes a
-// tile.  A workgroup's four waves take a tile's pages in turn and join in LDS.
+// Few rows a sequence.  All tiles of 16 RT rows lie one after the other on a
+// line, each with its pages and a constant for its start; with shares every
+// workgroup takes an equal part of it, whole tiles or pieces, whose parts a
+// second kernel joins; without, one workgroup takes a tile.  A workgroup's
+// four waves take a tile's pages in turn and join in LDS.
 // ---------------------------------------------------------------------------
 
 constexpr int kWaves = 4;
+constexpr int kStart = 4;   // pages that the start of a tile costs as much as
 
 struct Line {
-  int rows, unit_pages;   // rows of a tile; 1: counted in pages, 0: in tiles
+  int rows, pages_too;   // rows of a tile; 0: a tile counts 1
   __device__ __forceinline__ int tiles(const PagedArgs& a, int b) const {
     return (a.seq.tokens(b) * a.group + rows - 1) / rows;
   }
@@ -285,15 +295,11 @@ struct Line {
     return max(1, (a.seq.length(b) + kPage - 1) / kPage);
   }
   __device__ __forceinline__ int units(const PagedArgs& a, int b) const {
-    return tiles(a, b) * a.heads_k * (unit_pages ? pages(a, b) : 1);
+    return tiles(a, b) * a.heads_k * (pages_too ? kStart + pages(a, b) : 1);
   }
   __device__ __forceinline__ int total(const PagedArgs& a) const {
-    return before(a, a.seq.batch);
-  }
-  // of the first `n` sequences
-  __device__ __forceinline__ int before(const PagedArgs& a, int n) const {
     unsigned sum = 0;
-    for (int b = threadIdx.x & 63; b < n; b += 64) sum = add_sat(sum, units(a, b));
+    for (int b = threadIdx.x & 63; b < a.seq.batch; b += 64) sum = add_sat(sum, units(a, b));
 #pragma unroll
     for (int o = 32; o; o >>= 1) sum = add_sat(sum, __shfl_xor(sum, o));
     return __builtin_amdgcn_readfirstlane(min(sum, 0x7FFFFFFFu));
@@ -311,13 +317,20 @@ __device__ __forceinline__ Tile tile_at(const PagedArgs& a, int b, int x, int ro
   return t;
 }
 
-// the share of the line that workgroup w of a.groups takes: whole pages, but
-// at least kLeast, so that a workgroup's waves have one each
-constexpr int kLeast = 4;
-__device__ __forceinline__ int share_of(int total, int groups) { return max(kLeast, (total + groups - 1) / groups); }
-
-// floats of a part: O, m and l of a tile's rows
+// What the shares leave for the join: each workgroup's two parts (of a tile
+// that began before its share, and of one that begins in it and goes on), O, m
+// and l of a tile's rows, and a note on the latter tile.  (The 32 bytes of the
+// note spare the join the search for its tile.)
+struct Note {
+  int parts;             // 0: none
+  int rows, row0, h, start;   // the tile's rows, the first of them among its sequence's, key head, the sequence's first token
+  int unused[3];
+};
 __host__ __device__ constexpr int part_floats(int rows, int D) { return rows * (D + 2); }
+__device__ __forceinline__ Note* notes_of(const PagedArgs& a) { return reinterpret_cast<Note*>(a.part); }
+__device__ __forceinline__ float* part_of(const PagedArgs& a, int group, int second, int rows) {
+  return a.part + 8LL * a.groups + (2LL * group + second) * part_floats(rows, a.head_dim);
+}
 
 template <typename E, int DC, int RT>
 __global__ __launch_bounds__(kWaves * 64, 2) void k_paged_few(PagedArgs a) {
@@ -327,15 +340,19 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_paged_few(PagedArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int D = a.head_dim;
   pad(a, blockIdx.x, gridDim.x);
-  const Line line{kRows, a.part != nullptr};
-  int at = blockIdx.x, end = at + 1;   // in units of the line
-  if (a.part) {
-    const int total = line.total(a), share = share_of(total, a.groups);
-    if (static_cast<int64_t>(blockIdx.x) * share >= total) return;
-    at = blockIdx.x * share;
-    end = at + min(share, total - at);
+  const bool shares = a.part != nullptr;
+  const Line line{kRows, shares};
+  int64_t at = blockIdx.x, end = at + 1;   // in units of the line
+  int share = 1;
+  if (shares) {
+    const int total = line.total(a);
+    share = max(2 * kStart, total / a.groups + (total % a.groups != 0));
+    at *= share;
+    end = min(at + share, static_cast<int64_t>(total));
+    if (threadIdx.x == 0) notes_of(a)[blockIdx.x] = Note{};
+    if (at >= end) return;
   }
-  int b, in = at;   // the sequence, and the unit counted from its first
+  int b, in = static_cast<int>(at);   // the sequence, and the unit counted from its first
   if (!find(a.seq.batch, in, b, [&](int s) { return line.units(a, s); })) return;
   while (at < end) {
     const int units = line.units(a, b), pages = line.pages(a, b);
@@ -344,106 +361,130 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_paged_few(PagedArgs a) {
       if (++b >= a.seq.batch) return;
       continue;
     }
-    const int x = a.part ? in / pages : in, first = a.part ? in - x * pages : 0;
-    const int last = a.part ? min(pages, first + end - at) : pages;
-    const Tile t = tile_at(a, b, x, kRows);
-    const int rows = min(kRows, t.tokens * a.group - t.row0);
-    Rows<E, DC, RT> r;
-    r.init(a, t, 0);
-    r.walk(a, t, first + wave, last, kWaves, visible(a, t, 0));
-    // the waves' parts, joined in their order
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      float l = r.l[i];
-      l += __shfl_xor(l, 16);
-      l += __shfl_xor(l, 32);
-      const int row = i * 16 + r.l16;
-      if (r.g == 0) {
-        stats[wave][row][0] = r.m[i];
-        stats[wave][row][1] = l;
-      }
-#pragma unroll
-      for (int d = 0; d < 4 * DC; ++d) *reinterpret_cast<v4f*>(&out[wave][row][d * 16 + 4 * r.g]) = r.o[i][d];
+    int x = in, first = 0, last = pages, step = 1;
+    if (shares) {
+      const int size = kStart + pages;
+      x = in / size;
+      const int from = in - x * size, to = static_cast<int>(min(static_cast<int64_t>(size), from + end - at));
+      first = max(0, from - kStart);
+      last = max(0, to - kStart);
+      step = to - from;
     }
-    __syncthreads();
-    const bool whole = first == 0 && last == pages;
-    // a share's piece of a tile that began before it, or of one that goes on after it
-    float* const part = a.part ? a.part + (2LL * blockIdx.x + (first == 0)) * part_floats(kRows, D) : nullptr;
-    for (int e = threadIdx.x; e < rows * (D / 8); e += kWaves * 64) {
-      const int row = e / (D / 8), d = (e - row * (D / 8)) * 8;
-      float top = stats[0][row][0];
+    if (first < last) {
+      const Tile t = tile_at(a, b, x, kRows);
+      const int rows = min(kRows, t.tokens * a.group - t.row0);
+      Rows<E, DC, RT, true> r;
+      r.init(a, t, 0);
+      r.walk(a, t, first + wave, last, kWaves, visible(a, t, 0));
+      // the waves' parts, joined in their order
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, stats[w][row][0]);
-      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
+      for (int i = 0; i < RT; ++i) {
+        float l = r.l[i];
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        const int row = i * 16 + r.l16;
+        if (r.g == 0) {
+          stats[wave][row][0] = r.m[i];
+          stats[wave][row][1] = l;
+        }
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float s = exp2_fast(stats[w][row][0] - top);
-        l += s * stats[w][row][1];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) f[c] += s * out[w][row][d + c];
+        for (int d = 0; d < 4 * DC; ++d) *reinterpret_cast<v4f*>(&out[wave][row][d * 16 + 4 * r.g]) = r.o[i][d];
       }
-      if (whole) {
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      __syncthreads();
+      const bool whole = first == 0 && last == pages;
+      float* const part = shares ? part_of(a, blockIdx.x, first == 0, kRows) : nullptr;
+      if (!whole && first == 0 && threadIdx.x == 0) {
+        const int64_t after = (pages - last + static_cast<int64_t>(share) - 1) / share;   // shares that go on with it
+        notes_of(a)[blockIdx.x] = Note{static_cast<int>(min<int64_t>(after, a.groups - 1 - blockIdx.x)) + 1, rows, t.row0, t.h, t.start};
+      }
+      for (int e = threadIdx.x; e < rows * (D / 8); e += kWaves * 64) {
+        const int row = e / (D / 8), d = (e - row * (D / 8)) * 8;
+        float top = stats[0][row][0];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) f[c] *= inv;
-        put<E>(a, t, row, d, f);
-        if (d == 0) put_lse(a, t, row, top, l);
-      } else {
+        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, stats[w][row][0]);
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
 #pragma unroll
-        for (int c = 0; c < 8; c += 4) *reinterpret_cast<v4f*>(part + row * D + d + c) = v4f{f[c], f[c + 1], f[c + 2], f[c + 3]};
-        if (d == 0) {
-          part[kRows * D + 2 * row] = top;
-          part[kRows * D + 2 * row + 1] = l;
+        for (int w = 0; w < kWaves; ++w) {
+          const float s = exp2_fast(stats[w][row][0] - top);
+          l += s * stats[w][row][1];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) f[c] += s * out[w][row][d + c];
+        }
+        if (whole) {
+          const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) f[c] *= inv;
+          put<E>(a, t, row, d, f);
+          if (d == 0) put_lse(a, t, row, top, l);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; c += 4) *reinterpret_cast<v4f*>(part + row * D + d + c) = v4f{f[c], f[c + 1], f[c + 2], f[c + 3]};
+          if (d == 0) {
+            part[kRows * D + 2 * row] = top;
+            part[kRows * D + 2 * row + 1] = l;
+          }
         }
       }
+      __syncthreads();
     }
-    __syncthreads();
-    const int step = a.part ? last - first : 1;
     at += step;
     in += step;
   }
 }
 
-// The parts of a tile that shares cut, joined in their order: a workgroup a tile.
+// The parts of a tile that shares cut, joined in their order: a workgroup for
+// each that the note of a share names, a wave a row.  The first kAhead parts
+// are loaded beside their statistics: a chain of two loads, as a part's way
+// from another XCD's L2 takes 2 us.
 template <typename E, int RT>
 __global__ __launch_bounds__(256) void k_paged_join(PagedArgs a) {
-  constexpr int kRows = 16 * RT;
-  const int D = a.head_dim;
-  const Line line{kRows, 1}, whole{kRows, 0};
-  const int share = share_of(line.total(a), a.groups);
-  int b, x = blockIdx.x;
-  if (!find(a.seq.batch, x, b, [&](int s) { return whole.units(a, s); })) return;
-  const int pages = line.pages(a, b);
-  const int64_t from = static_cast<int64_t>(line.before(a, b)) + static_cast<int64_t>(x) * pages;
-  const int64_t g0 = from / share, g1 = (from + pages - 1) / share;
-  if (g0 == g1 || g1 >= a.groups) return;   // one workgroup had it whole; starts that overlap
-  const Tile t = tile_at(a, b, x, kRows);
-  const int rows = min(kRows, t.tokens * a.group - t.row0);
-  const int64_t size = part_floats(kRows, D);
-  // the first part begins the tile, the others go on with it
-  auto part = [&](int64_t g) { return a.part + (2 * g + (g == g0)) * size; };
-  for (int e = threadIdx.x; e < rows * (D / 8); e += 256) {
-    const int row = e / (D / 8), d = (e - row * (D / 8)) * 8;
-    float top = kNothing;
-    for (int64_t g = g0; g <= g1; ++g) top = fmaxf(top, part(g)[kRows * D + 2 * row]);
-    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
-#pragma unroll 4
-    for (int64_t g = g0; g <= g1; ++g) {
-      const float* const p = part(g);
-      const float s = exp2_fast(p[kRows * D + 2 * row] - top);
-      l += s * p[kRows * D + 2 * row + 1];
-      const v4f lo = *reinterpret_cast<const v4f*>(p + row * D + d), hi = *reinterpret_cast<const v4f*>(p + row * D + d + 4);
+  constexpr int kRows = 16 * RT, kAhead = 24;
+  const int D = a.head_dim, lane = threadIdx.x & 63, g0 = blockIdx.x;
+  const Note note = notes_of(a)[g0];
+  const int parts = note.parts;
+  auto part = [&](int i) { return part_of(a, g0 + i, i == 0, kRows); };
+  const int d = min(2 * lane, D - 2);   // lanes past the row repeat its end
+  for (int row = threadIdx.x >> 6; parts && row < note.rows; row += 4) {
+    auto values = [&](int i) { return *reinterpret_cast<const v2f*>(part(i) + row * D + d); };
+    v2f ahead[kAhead];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        f[c] += s * lo[c];
-        f[4 + c] += s * hi[c];
+    for (int i = 0; i < kAhead; ++i) ahead[i] = values(min(i, parts - 1));
+    float top = kNothing;
+    for (int i = lane; i < parts; i += 64) top = fmaxf(top, part(i)[kRows * D + 2 * row]);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    float f[2] = {0.f, 0.f}, l = 0.f;
+    for (int i0 = 0; i0 < parts; i0 += 64) {
+      float s = 0.f, sum = 0.f;
+      if (i0 + lane < parts) {
+        const float* const p = part(i0 + lane) + kRows * D + 2 * row;
+        s = exp2_fast(p[0] - top);
+        sum = s * p[1];
       }
+      auto add = [&](int i, v2f v) {
+        const float si = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s), i));
+        l += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sum), i));
+        f[0] += si * v[0];
+        f[1] += si * v[1];
+      };
+      const int n = min(64, parts - i0);
+      int i = 0;
+      if (i0 == 0) {
+#pragma unroll
+        for (; i < kAhead; ++i)
+          if (i < n) add(i, ahead[i]);
+      }
+#pragma unroll 8
+      for (; i < n; ++i) add(i, values(i0 + i));
     }
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) f[c] *= inv;
-    put<E>(a, t, row, d, f);
-    if (d == 0) put_lse(a, t, row, top, l);
+    const int all = note.row0 + row, token = all / a.group, head = note.h * a.group + all - token * a.group;
+    if (2 * lane < D) {
+      const uint32_t v = E::pack2(f[0] * inv, f[1] * inv);
+      __builtin_memcpy(a.o + (note.start + token) * a.ldo + head * a.hdo + d, &v, 4);
+    }
+    if (lane == 0 && a.lse)
+      a.lse[static_cast<int64_t>(note.start + token) * a.heads_q + head] = logarithm(top, l);
   }
 }
 
@@ -463,7 +504,7 @@ __global__ __launch_bounds__(256, 2) void k_paged_many(PagedArgs a) {
   const Tile t = tile_at(a, b, x, kRows);
   const int left = t.tokens * a.group - t.row0, r0 = wave * 32;
   if (r0 >= left) return;
-  Rows<E, DC, RT> r;
+  Rows<E, DC, RT, false> r;
   r.init(a, t, r0);
   const int most = visible(a, t, min(r0 + 31, left - 1));
   r.walk(a, t, 0, (most + kPage - 1) / kPage, 1, visible(a, t, r0));
@@ -501,7 +542,7 @@ Plan plan_for(int total, int batch, int width, int heads_q, int heads_k, int D) 
     // up to 1024 keys a workgroup has them soon; past that every CU takes its share
     if (width > 16) {
       p.groups = 2 * kCUs;
-      p.bytes = 2 * static_cast<size_t>(p.groups) * part_floats(p.rows, D) * 4;
+      p.bytes = static_cast<size_t>(p.groups) * (sizeof(Note) + 2 * sizeof(float) * part_floats(p.rows, D));
     }
   }
   return p;
@@ -519,9 +560,9 @@ void start(const PagedArgs& a, const Plan& p, hipStream_t stream) {
     k_paged_few<E, DC, 2><<<blocks, kWaves * 64, 0, stream>>>(a);
   if (!a.part) return;
   if (p.rows == 16)
-    k_paged_join<E, 1><<<tiles, 256, 0, stream>>>(a);
+    k_paged_join<E, 1><<<a.groups, 256, 0, stream>>>(a);
   else
-    k_paged_join<E, 2><<<tiles, 256, 0, stream>>>(a);
+    k_paged_join<E, 2><<<a.groups, 256, 0, stream>>>(a);
 }
 
 template <typename E>
