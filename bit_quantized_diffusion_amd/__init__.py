@@ -26,7 +26,7 @@ from ._lib import (BF16, F16, INT4, MXFP4, SVDQ_ERR_HIP, SVDQ_ERR_INVALID_ARG,  
 from .block_ops import (attention, attention_workspace_size, layer_norm, linear16,  # noqa: F401
                         linear16_workspace_size, rms_norm)
 from .fp8_ops import (FP8_BLOCK, PAGE, KVCache, attention_paged, attention_paged_workspace_size,  # noqa: F401
-                      cache_append, gemm_fp8, gemm_fp8_workspace_size, linear_fp8, pack_fp8,
+                      cache_append, gemm_fp8, linear_fp8, pack_fp8,
                       quantize_fp8, rms_norm_fp8, rope_table)
 
 __all__ = [
@@ -38,7 +38,7 @@ __all__ = [
     "pack_w4a16", "gemm_w4a16", "mfma_ceiling",
     "BF16", "F16", "attention", "attention_workspace_size", "linear16",
     "linear16_workspace_size", "layer_norm", "rms_norm",
-    "FP8_BLOCK", "pack_fp8", "quantize_fp8", "rms_norm_fp8", "gemm_fp8", "gemm_fp8_workspace_size", "linear_fp8",
+    "FP8_BLOCK", "pack_fp8", "quantize_fp8", "rms_norm_fp8", "gemm_fp8", "linear_fp8",
     "PAGE", "KVCache", "rope_table", "cache_append", "attention_paged", "attention_paged_workspace_size",
 ]
 

@@ -35,7 +35,7 @@ EXPORTED = (
     "svdq_attention_workspace_size", "svdq_attention",
     "svdq_linear16_workspace_size", "svdq_linear16_workspace_size_for", "svdq_linear16", "svdq_layer_norm",
     "svdq_debug_attention_plan", "svdq_debug_linear16_plan",
-    "svdq_rms_norm", "svdq_quantize_fp8", "svdq_pack_fp8", "svdq_gemm_fp8_workspace_size", "svdq_gemm_fp8",
+    "svdq_rms_norm", "svdq_quantize_fp8", "svdq_pack_fp8", "svdq_gemm_fp8",
     "svdq_debug_gemm_fp8_plan", "svdq_cache_append", "svdq_attention_paged_workspace_size", "svdq_attention_paged",
     "svdq_debug_attention_paged_plan",
 )
@@ -90,8 +90,7 @@ def _load():
         "svdq_rms_norm": ([vp, l, vp, l, vp, vp, l, vp, l, vp, vp, i, i, ctypes.c_float, i, vp], i),
         "svdq_quantize_fp8": ([vp, l, vp, vp, i, i, i, vp], i),
         "svdq_pack_fp8": ([vp, i, i, i, vp, vp], i),
-        "svdq_gemm_fp8_workspace_size": ([i, i, i, sz], i),
-        "svdq_gemm_fp8": ([vp, vp, vp, vp, vp, vp, l, i, vp, l, vp, l, i, i, i, i, i, vp, ctypes.c_size_t, vp], i),
+        "svdq_gemm_fp8": ([vp, vp, vp, vp, vp, vp, l, i, vp, l, vp, l, i, i, i, i, i, vp], i),
         "svdq_debug_gemm_fp8_plan": ([i, i, i, vp], i),
         "svdq_cache_append": ([vp, vp, vp, vp, vp, vp, vp, vp, i, vp, i, vp, vp, i, i, i, i, i, vp, i, i, i, i, vp], i),
         "svdq_attention_paged_workspace_size": ([i, i, i, i, i, i, sz], i),

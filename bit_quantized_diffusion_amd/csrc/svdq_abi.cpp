@@ -474,18 +474,9 @@ int svdq_quantize_fp8(const void* x, int64_t ldx, uint8_t* xq, float* xs, int M,
   return hip_status(svdq_launch_quantize_fp8(x, ldx, xq, xs, M, K, dtype, stream));
 }
 
-int svdq_gemm_fp8_workspace_size(int M, int N, int K, size_t* out_bytes) {
-  if (!out_bytes) return SVDQ_ERR_INVALID_ARG;
-  *out_bytes = 0;
-  const int st = check_gemm_fp8_shape(M, N, K);
-  if (st) return st;
-  *out_bytes = svdq_gemm_fp8_plan_bytes(M, N, K);
-  return SVDQ_OK;
-}
-
 int svdq_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const void* bias, const void* gate,
                   int64_t ld_gate, int group_rows, const void* residual, int64_t ldr, void* y, int64_t ldy, int M, int N,
-                  int K, int activation, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+                  int K, int activation, int dtype, void* stream) {
   int st = check_dtype(dtype);
   if (st) return st;
   if (activation != SVDQ_ACT_NONE && activation != SVDQ_ACT_GELU && activation != SVDQ_ACT_SILU)
@@ -493,12 +484,12 @@ int svdq_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const f
   if ((st = check_gemm_fp8_shape(M, N, K))) return st;
   if (!xq || !xs || !wq || !ws || !y) return SVDQ_ERR_INVALID_ARG;
   if (!aligned16(xq) || !aligned4(xs) || !aligned16(wq) || !aligned4(ws) || !aligned2(y) || !aligned2(bias) ||
-      !aligned2(gate) || !aligned2(residual) || !aligned16(workspace))
+      !aligned2(gate) || !aligned2(residual))
     return SVDQ_ERR_INVALID_ARG;
   if (ldy < N || (residual && ldr < N) || (gate && (ld_gate < N || group_rows < 1))) return SVDQ_ERR_SHAPE;
   if ((st = current_device_ok())) return st;
   return hip_status(svdq_launch_gemm_fp8(xq, xs, wq, ws, bias, gate, ld_gate, group_rows < 1 ? 1 : group_rows, residual, ldr,
-                                         y, ldy, M, N, K, activation, dtype, workspace, workspace_bytes, stream));
+                                         y, ldy, M, N, K, activation, dtype, stream));
 }
 
 int svdq_cache_append(const void* q, const void* k, const void* v, void* q_out, const int64_t* strides, uint8_t* k_cache,

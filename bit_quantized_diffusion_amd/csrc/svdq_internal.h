@@ -102,12 +102,10 @@ int svdq_launch_rms_norm(const void* x, int64_t ldx, const void* residual, int64
                          int64_t ld_sum, void* y, int64_t ldy, uint8_t* yq, float* ys, int M, int K, float eps, int dtype,
                          void* stream);
 int svdq_launch_quantize_fp8(const void* x, int64_t ldx, uint8_t* xq, float* xs, int M, int K, int dtype, void* stream);
-size_t svdq_gemm_fp8_plan_bytes(int M, int N, int K);
 void svdq_gemm_fp8_plan(int M, int N, int K, int32_t* plan);
 int svdq_launch_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const void* bias,
                          const void* gate, int64_t ld_gate, int group_rows, const void* residual, int64_t ldr, void* y,
-                         int64_t ldy, int M, int N, int K, int activation, int dtype, void* workspace,
-                         size_t workspace_bytes, void* stream);
+                         int64_t ldy, int M, int N, int K, int activation, int dtype, void* stream);
 int svdq_launch_cache_append(const void* q, const void* k, const void* v, void* q_out, const int64_t* strides,
                              uint8_t* k_cache, uint8_t* v_cache, int8_t* exponents, int pages, const int32_t* table,
                              int width, const int32_t* lengths, const int32_t* cu, int batch, int total, int heads_q,

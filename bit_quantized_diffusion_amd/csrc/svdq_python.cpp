@@ -589,10 +589,10 @@ PyObject* quantize_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return PyTuple_Pack(2, xq.get(), xs.get());
 }
 
-// gemm_fp8(xq, xs, wq, ws, bias, activation code, gate, residual, group_rows, dtype, out, workspace), and with
-// xs None, xq being 16-bit activations: their codes are made first
+// gemm_fp8(xq, xs, wq, ws, bias, activation code, gate, residual, group_rows, dtype, out), and with xs None, xq
+// being 16-bit activations: their codes are made first
 PyObject* gemm_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (!count_of("gemm_fp8", n, 12)) return nullptr;
+  if (!count_of("gemm_fp8", n, 11)) return nullptr;
   Tensor x, xs, wq, ws, bias, residual, y, like_y;
   int code;
   const bool whole = args[1] == Py_None;
@@ -644,11 +644,7 @@ PyObject* gemm_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (!out) return nullptr;
   if (M == 0) return out.release();
   const int m = static_cast<int>(M), nn = static_cast<int>(N), k = static_cast<int>(K);
-  size_t bytes = 0, size;
-  if (args[11] != Py_None && !fine(svdq_gemm_fp8_workspace_size(m, nn, k, &bytes))) return nullptr;
-  void* space;
-  Ref keep, codes;
-  if (!workspace_of(args[11], args[0], x, bytes, space, size, keep)) return nullptr;
+  Ref codes;
   uint8_t* q = static_cast<uint8_t*>(x.ptr);
   float* s = static_cast<float*>(xs.ptr);
   if (whole) {
@@ -663,7 +659,7 @@ PyObject* gemm_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
           if (const int st = svdq_quantize_fp8(x.ptr, x.ld(), q, s, m, k, code, stream)) return st;
         return svdq_gemm_fp8(q, s, static_cast<uint8_t*>(wq.ptr), static_cast<float*>(ws.ptr), bias.ptr, gate.ptr, gate.ld,
                              static_cast<int>(gate.rows), residual.ptr, residual.ptr ? residual.ld() : 0, y.ptr, y.ld(), m,
-                             nn, k, static_cast<int>(act), code, space, size, stream);
+                             nn, k, static_cast<int>(act), code, stream);
       }))
     return nullptr;
   return out.release();

@@ -48,14 +48,6 @@ def rms_norm_fp8(x, weight=None, *, residual=None, eps: float = 1e-6, residual_o
     return _block_ops.rms_norm(x, weight, residual, eps, None, residual_out, True)
 
 
-def gemm_fp8_workspace_size(M: int, N: int, K: int) -> int:
-    """Bytes of workspace with which `gemm_fp8` cuts small grids along K (0: it
-    runs them in one piece anyway)."""
-    out = ctypes.c_size_t(0)
-    check(lib.svdq_gemm_fp8_workspace_size(M, N, K, ctypes.byref(out)))
-    return int(out.value)
-
-
 def _activation(name: str) -> int:
     act = ACTIVATIONS.get(name)
     if act is None:
@@ -64,19 +56,18 @@ def _activation(name: str) -> int:
 
 
 def gemm_fp8(xq, xs, wq, ws, bias=None, *, dtype=torch.bfloat16, activation: str = "none", gate=None, residual=None,
-             group_rows=None, out=None, workspace="auto"):
+             group_rows=None, out=None):
     """residual + gate * act(x w^T + bias) from codes and scales of x
     (`quantize_fp8`, `rms_norm_fp8`) and w (`pack_fp8`), in `dtype` (bfloat16
     or float16; bias, gate, residual and `out` have it too).  Epilogue,
-    `group_rows`, `out` and workspace as for `linear16`.  No gradient."""
-    return _block_ops.gemm_fp8(xq, xs, wq, ws, bias, _activation(activation), gate, residual, group_rows, dtype, out, workspace)
+    `group_rows` and `out` as for `linear16`.  No gradient."""
+    return _block_ops.gemm_fp8(xq, xs, wq, ws, bias, _activation(activation), gate, residual, group_rows, dtype, out)
 
 
-def linear_fp8(x, wq, ws, bias=None, *, activation: str = "none", gate=None, residual=None, group_rows=None, out=None,
-               workspace="auto"):
+def linear_fp8(x, wq, ws, bias=None, *, activation: str = "none", gate=None, residual=None, group_rows=None, out=None):
     """`gemm_fp8` of 16-bit activations x [M][K], whose codes are made on the
     way (`quantize_fp8`); the result has x's dtype."""
-    return _block_ops.gemm_fp8(x, None, wq, ws, bias, _activation(activation), gate, residual, group_rows, None, out, workspace)
+    return _block_ops.gemm_fp8(x, None, wq, ws, bias, _activation(activation), gate, residual, group_rows, None, out)
 
 
 @dataclass

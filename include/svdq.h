@@ -485,22 +485,16 @@ SVDQ_API int svdq_pack_fp8(const uint16_t* w, int K, int N, int dtype, uint8_t* 
  *
  * xq, xs, wq, ws (dev) as above, xs and ws 4-byte aligned; bias, gate,
  * residual, y, activation and dtype (theirs) as for svdq_linear16.  Sums are
- * fp32, the blocks' in their order, but that the matrix core takes the 8-bit
+ * fp32, the blocks' in a fixed order, but that the matrix core takes the 8-bit
  * products of 8 consecutive k to the largest one's exponent E and cuts what
  * lies below 2^(E - 13) (about 1e-4 of a result of 4096 products); y is
  * rounded once and overlaps no operand but residual.
  * M, N >= 1, M at most 2^31 - 2^16, N at most 2^28 - 32, fewer than 2^24 tiles
  * of 64 x 64 in the result; K a multiple of 16 to 2^22.
- * workspace (dev, 16-byte aligned): with the bytes that
- * svdq_gemm_fp8_workspace_size names, grids that would leave the device idle
- * are cut along K into fp32 parts that a second kernel adds in a fixed order;
- * with NULL or fewer bytes they run in one piece.  Results are
- * deterministic. */
-SVDQ_API int svdq_gemm_fp8_workspace_size(int M, int N, int K, size_t* out_bytes);
+ * Results are deterministic. */
 SVDQ_API int svdq_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const void* bias,
                               const void* gate, int64_t ld_gate, int group_rows, const void* residual, int64_t ldr,
-                              void* y, int64_t ldy, int M, int N, int K, int activation, int dtype, void* workspace,
-                              size_t workspace_bytes, void* stream);
+                              void* y, int64_t ldy, int M, int N, int K, int activation, int dtype, void* stream);
 
 /* Keys and values of packed sequences in a paged cache of 8-bit codes.
  *
@@ -615,7 +609,7 @@ SVDQ_API int svdq_debug_group_partials(const uint8_t* xq, const uint8_t* wq,
  *   linear16: plan[0] rows and [1] channels of a tile, [2] waves of a
  *   workgroup, [3] splits along K; aligned != 0: rows of x and w are 16-byte
  *   aligned, which takes K % 8 == 0
- *   gemm_fp8: as for linear16
+ *   gemm_fp8: plan[0] to [2] as for linear16
  *   attention_paged: plan[0] rows of a tile, [1] workgroups that take equal
  *   shares of all keys (0: a tile's keys are one workgroup's) */
 SVDQ_API int svdq_debug_attention_plan(int total_q, int total_k, int batch, int heads_q,

@@ -25,7 +25,7 @@ NORM = dict(x=FAKE, ldx=64, residual=FAKE, ldr=64, weight=FAKE, sum=FAKE, ld_sum
 CODES = dict(NORM, y=None, yq=FAKE, ys=FAKE)
 QUANT = dict(x=FAKE, ldx=64, xq=FAKE, xs=FAKE, m=8, k=64, dtype=0)
 GEMM = dict(xq=FAKE, xs=FAKE, wq=FAKE, ws=FAKE, bias=FAKE, gate=FAKE, ld_gate=32, rows=4, residual=FAKE, ldr=32, y=FAKE, ldy=32, m=8,
-            n=32, k=64, act=0, dtype=0, ws_=None, size=0)
+            n=32, k=64, act=0, dtype=0)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -53,7 +53,7 @@ def test_quantize_refuses(kw, want):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(xq=None), BAD), (dict(xs=None), BAD), (dict(wq=None), BAD), (dict(ws=None), BAD), (dict(y=None), BAD), (dict(xq=OFF), BAD),
-    (dict(wq=OFF), BAD), (dict(xs=ODD), BAD), (dict(ws=ODD), BAD), (dict(y=ODD), BAD), (dict(residual=ODD), BAD), (dict(ws_=OFF), BAD),
+    (dict(wq=OFF), BAD), (dict(xs=ODD), BAD), (dict(ws=ODD), BAD), (dict(y=ODD), BAD), (dict(residual=ODD), BAD),
     (dict(act=3), BAD), (dict(dtype=-1), BAD), (dict(m=0), SHAPE), (dict(n=0), SHAPE), (dict(k=0), SHAPE), (dict(k=72), SHAPE),
     (dict(k=(1 << 22) + 16), SHAPE), (dict(ldy=31), SHAPE), (dict(ldr=31), SHAPE), (dict(ld_gate=31), SHAPE), (dict(rows=0), SHAPE),
     (dict(m=2 ** 31 - 100), SHAPE), (dict(n=2 ** 28, ldy=2 ** 28, ldr=2 ** 28, ld_gate=2 ** 28), SHAPE),
@@ -63,13 +63,17 @@ def test_gemm_refuses(kw, want):
     assert bq.lib.svdq_gemm_fp8(*dict(GEMM, **kw).values(), None) == want
 
 
-def test_workspace_and_plan():
-    out, plan = ctypes.c_size_t(7), (ctypes.c_int32 * 4)()
-    assert bq.lib.svdq_gemm_fp8_workspace_size(1, 1, 16, None) == BAD and bq.lib.svdq_debug_gemm_fp8_plan(1, 1, 16, None) == BAD
-    assert bq.lib.svdq_gemm_fp8_workspace_size(1, 1, 24, ctypes.byref(out)) == SHAPE and out.value == 0
-    assert bq.lib.svdq_debug_gemm_fp8_plan(0, 1, 16, plan) == SHAPE
-    assert bq.gemm_fp8_workspace_size(4608, 12288, 4096) == 0 and bq.gemm_fp8_workspace_size(8, 64, 4096) == 0
-    assert bq.gemm_fp8_workspace_size(100, 256, 8192) % (100 * 256 * 4) == 0
+def test_plan_refuses():
+    plan = (ctypes.c_int32 * 3)()
+    assert bq.lib.svdq_debug_gemm_fp8_plan(1, 1, 16, None) == BAD
+    assert bq.lib.svdq_debug_gemm_fp8_plan(0, 1, 16, plan) == SHAPE and bq.lib.svdq_debug_gemm_fp8_plan(1, 1, 24, plan) == SHAPE
+
+
+def test_gemm_sizes_reach_every_tile_shape():
+    from tests import test_gpu_gemm_fp8 as gemm
+    for case, want in gemm.SHAPES.items():
+        assert gemm.plan(*case) == want, case
+    assert len(set(gemm.SHAPES.values())) == len(gemm.SHAPES) == 14
 
 
 @pytest.mark.skipif(_gpu_present(), reason="checks the no-device path")
