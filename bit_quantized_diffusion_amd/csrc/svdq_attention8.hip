@@ -23,6 +23,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "svdq_internal.h"
 #include "svdq_cache.h"
 
@@ -311,9 +313,9 @@ __device__ __forceinline__ Tile tile_at(const PagedArgs& a, int b, int x, int ro
   t.b = b;
   t.h = x % a.heads_k;
   t.row0 = x / a.heads_k * rows;
-  t.tokens = a.seq.tokens(b);
-  t.length = a.seq.length(b);
-  t.start = a.seq.start(b);
+  t.tokens = __builtin_amdgcn_readfirstlane(a.seq.tokens(b));
+  t.length = __builtin_amdgcn_readfirstlane(a.seq.length(b));
+  t.start = __builtin_amdgcn_readfirstlane(a.seq.start(b));
   return t;
 }
 
@@ -332,13 +334,73 @@ __device__ __forceinline__ float* part_of(const PagedArgs& a, int group, int sec
   return a.part + 8LL * a.groups + (2LL * group + second) * part_floats(rows, a.head_dim);
 }
 
+// LDS in which NW waves join their parts of 16 RT rows.
+template <int DC, int RT, int NW>
+struct Joined {
+  float o[NW][16 * RT][64 * DC + 4];
+  float stats[NW][16 * RT][2];   // m, l
+};
+
+// NW waves take pages first, first + 1, ... before last of a tile in turn and
+// join: the result itself, or (part) a share's part of it.
+template <typename E, int DC, int RT, int NW>
+__device__ __forceinline__ void few_rows(const PagedArgs& a, const Tile& t, int first, int last, float* part, Joined<DC, RT, NW>& lds) {
+  constexpr int kRows = 16 * RT;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), D = a.head_dim;
+  const int rows = min(kRows, t.tokens * a.group - t.row0);
+  Rows<E, DC, RT, true> r;
+  r.init(a, t, 0);
+  r.walk(a, t, first + wave, last, NW, visible(a, t, 0));
+  // the waves' parts, joined in their order
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    float l = r.l[i];
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    const int row = i * 16 + r.l16;
+    if (r.g == 0) {
+      lds.stats[wave][row][0] = r.m[i];
+      lds.stats[wave][row][1] = l;
+    }
+#pragma unroll
+    for (int d = 0; d < 4 * DC; ++d) *reinterpret_cast<v4f*>(&lds.o[wave][row][d * 16 + 4 * r.g]) = r.o[i][d];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < rows * (D / 8); e += NW * 64) {
+    const int row = e / (D / 8), d = (e - row * (D / 8)) * 8;
+    float top = lds.stats[0][row][0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) top = fmaxf(top, lds.stats[w][row][0]);
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float s = exp2_fast(lds.stats[w][row][0] - top);
+      l += s * lds.stats[w][row][1];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) f[c] += s * lds.o[w][row][d + c];
+    }
+    if (!part) {
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) f[c] *= inv;
+      put<E>(a, t, row, d, f);
+      if (d == 0) put_lse(a, t, row, top, l);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; c += 4) *reinterpret_cast<v4f*>(part + row * D + d + c) = v4f{f[c], f[c + 1], f[c + 2], f[c + 3]};
+      if (d == 0) {
+        part[kRows * D + 2 * row] = top;
+        part[kRows * D + 2 * row + 1] = l;
+      }
+    }
+  }
+  __syncthreads();
+}
+
 template <typename E, int DC, int RT>
 __global__ __launch_bounds__(kWaves * 64, 2) void k_paged_few(PagedArgs a) {
-  constexpr int kRows = 16 * RT, kD = 64 * DC, kLd = kD + 4;
-  __shared__ __attribute__((aligned(16))) float out[kWaves][kRows][kLd];
-  __shared__ float stats[kWaves][kRows][2];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int D = a.head_dim;
+  constexpr int kRows = 16 * RT;
+  __shared__ __attribute__((aligned(16))) Joined<DC, RT, kWaves> lds;
   pad(a, blockIdx.x, gridDim.x);
   const bool shares = a.part != nullptr;
   const Line line{kRows, shares};
@@ -372,60 +434,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_paged_few(PagedArgs a) {
     }
     if (first < last) {
       const Tile t = tile_at(a, b, x, kRows);
-      const int rows = min(kRows, t.tokens * a.group - t.row0);
-      Rows<E, DC, RT, true> r;
-      r.init(a, t, 0);
-      r.walk(a, t, first + wave, last, kWaves, visible(a, t, 0));
-      // the waves' parts, joined in their order
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        float l = r.l[i];
-        l += __shfl_xor(l, 16);
-        l += __shfl_xor(l, 32);
-        const int row = i * 16 + r.l16;
-        if (r.g == 0) {
-          stats[wave][row][0] = r.m[i];
-          stats[wave][row][1] = l;
-        }
-#pragma unroll
-        for (int d = 0; d < 4 * DC; ++d) *reinterpret_cast<v4f*>(&out[wave][row][d * 16 + 4 * r.g]) = r.o[i][d];
-      }
-      __syncthreads();
       const bool whole = first == 0 && last == pages;
-      float* const part = shares ? part_of(a, blockIdx.x, first == 0, kRows) : nullptr;
       if (!whole && first == 0 && threadIdx.x == 0) {
         const int64_t after = (pages - last + static_cast<int64_t>(share) - 1) / share;   // shares that go on with it
-        notes_of(a)[blockIdx.x] = Note{static_cast<int>(min<int64_t>(after, a.groups - 1 - blockIdx.x)) + 1, rows, t.row0, t.h, t.start};
+        notes_of(a)[blockIdx.x] = Note{static_cast<int>(min<int64_t>(after, a.groups - 1 - blockIdx.x)) + 1,
+                                       min(kRows, t.tokens * a.group - t.row0), t.row0, t.h, t.start};
       }
-      for (int e = threadIdx.x; e < rows * (D / 8); e += kWaves * 64) {
-        const int row = e / (D / 8), d = (e - row * (D / 8)) * 8;
-        float top = stats[0][row][0];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, stats[w][row][0]);
-        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          const float s = exp2_fast(stats[w][row][0] - top);
-          l += s * stats[w][row][1];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) f[c] += s * out[w][row][d + c];
-        }
-        if (whole) {
-          const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) f[c] *= inv;
-          put<E>(a, t, row, d, f);
-          if (d == 0) put_lse(a, t, row, top, l);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 8; c += 4) *reinterpret_cast<v4f*>(part + row * D + d + c) = v4f{f[c], f[c + 1], f[c + 2], f[c + 3]};
-          if (d == 0) {
-            part[kRows * D + 2 * row] = top;
-            part[kRows * D + 2 * row + 1] = l;
-          }
-        }
-      }
-      __syncthreads();
+      few_rows<E, DC, RT, kWaves>(a, t, first, last, whole ? nullptr : part_of(a, blockIdx.x, first == 0, kRows), lds);
     }
     at += step;
     in += step;
@@ -468,14 +483,13 @@ __global__ __launch_bounds__(256) void k_paged_join(PagedArgs a) {
         f[1] += si * v[1];
       };
       const int n = min(64, parts - i0);
-      int i = 0;
       if (i0 == 0) {
 #pragma unroll
-        for (; i < kAhead; ++i)
+        for (int i = 0; i < kAhead; ++i)
           if (i < n) add(i, ahead[i]);
       }
 #pragma unroll 8
-      for (; i < n; ++i) add(i, values(i0 + i));
+      for (int i = i0 ? 0 : kAhead; i < n; ++i) add(i, values(i0 + i));
     }
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
     const int all = note.row0 + row, token = all / a.group, head = note.h * a.group + all - token * a.group;
@@ -489,43 +503,302 @@ __global__ __launch_bounds__(256) void k_paged_join(PagedArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Many rows a sequence (chunks of prompts): 32 rows a wave, 128 a workgroup,
-// each wave through all pages that its rows see.
+// Many rows a sequence (chunks of prompts): NW waves of 32 rows share pages.
+// Bound by the matrix core and the exponentials.  A page's codes are loaded
+// into registers, widened once for all waves and put into LDS, from where they
+// are the products' operands, of 32 x 32 x 16 here.
+//
+// Iteration i has two phases, in each of which matrix and vector work stand
+// side by side in the instruction order:
+//   A  S of page i + 1, beside most weights of page i
+//   B  O += P V of page i, beside the last weights, the maxima of page i + 1,
+//      and the widening of K of page i + 2 and V of page i + 1
+// Operands are read from LDS kAhead products ahead; codes are loaded an
+// iteration before they are widened.  Two buffers each for K and V, one
+// barrier a page.  Past the last page the work goes on with what the buffers
+// hold, and nothing of it is used: no branch parts the products from the
+// vector work.  The running reference moves only when a row's maximum passes
+// it by 2^8.
+//
+// K's rows in LDS are 128 DC bytes, 16-byte chunk c of row r at
+// c ^ (r % (8 DC)); V lies as the lanes read it: 16 bytes for each of 16 keys,
+// 32 dimensions and lane.
 // ---------------------------------------------------------------------------
 
-template <typename E, int DC>
-__global__ __launch_bounds__(256, 2) void k_paged_many(PagedArgs a) {
-  constexpr int RT = 2, kRows = 128;
+template <typename E, int DC, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void k_paged_many(PagedArgs a) {
+  constexpr int kRows = NW * 32, kThreads = NW * 64, kDims = 64 * DC, kTile = kPage * kDims * 2;
+  constexpr int kChunks = kPage * kDims / 16 / kThreads;   // of 16 codes, a thread's
+  constexpr int kSteps = kDims / 16, kDt = kDims / 32, kProducts = 2 * kSteps, kAhead = 4, kWeights = 16, kLate = 4;
+  constexpr float kSlack = 8.f;
+  static_assert(kChunks >= 1 && kProducts == 4 * kDt, "work divides evenly");
+  using Few = Joined<DC, 1, NW>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[sizeof(Few) > 4 * kTile ? sizeof(Few) : 4 * kTile];   // K, K, V, V
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int D = a.head_dim;
   pad(a, blockIdx.x, gridDim.x);
   const Line line{kRows, 0};
   int b, x = blockIdx.x;
   if (!find(a.seq.batch, x, b, [&](int s) { return line.units(a, s); })) return;
+  // a sequence's last rows see the most keys: they come first
+  x = line.tiles(a, b) * a.heads_k - 1 - x;
   const Tile t = tile_at(a, b, x, kRows);
   const int left = t.tokens * a.group - t.row0, r0 = wave * 32;
-  if (r0 >= left) return;
-  Rows<E, DC, RT, false> r;
-  r.init(a, t, r0);
-  const int most = visible(a, t, min(r0 + 31, left - 1));
-  r.walk(a, t, 0, (most + kPage - 1) / kPage, 1, visible(a, t, r0));
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    float l = r.l[i];
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    const int row = r0 + i * 16 + r.l16;
-    if (row >= left) continue;
-    if (r.g == 0) put_lse(a, t, row, r.m[i], l);
-    const int all = t.row0 + row, token = all / a.group, head = t.h * a.group + all - token * a.group;
-    uint16_t* const o = a.o + (t.start + token) * a.ldo + head * a.hdo + 4 * r.g;
-#pragma unroll
-    for (int d = 0; d < 4 * DC; ++d)
-      if (d * 16 < a.head_dim) {
-        const v2u v = {E::pack2(r.o[i][d][0] * inv, r.o[i][d][1] * inv), E::pack2(r.o[i][d][2] * inv, r.o[i][d][3] * inv)};
-        __builtin_memcpy(o + d * 16, &v, 8);
-      }
+  if (left <= 32) {   // a wave's rows: the waves share its pages instead
+    Tile part = t;
+    for (; part.row0 < t.tokens * a.group; part.row0 += 16)
+      few_rows<E, DC, 1, NW>(a, part, 0, line.pages(a, b), nullptr, *reinterpret_cast<Few*>(lds));
+    return;
   }
+  const int last = (visible(a, t, min(kRows, left) - 1) + kPage - 1) / kPage;   // pages that the tile's rows see
+  const int every = visible(a, t, r0);                                          // keys that each of the wave's sees
+  const bool idle = r0 >= left;
+
+  // the lane's row
+  const int r = r0 + l32, row = t.row0 + r, token = row / a.group, head = t.h * a.group + row - token * a.group;
+  const bool valid = r < left;
+  const int sees = visible(a, t, r);
+  v4u q[kSteps];
+#pragma unroll
+  for (int st = 0; st < kSteps; ++st) {
+    const int d = 16 * st + 8 * h;
+    q[st] = valid && d < D ? load8(a.q + (t.start + token) * a.ldq + head * a.hdq + d) : v4u{0, 0, 0, 0};
+  }
+  v16f o[kDt];
+#pragma unroll
+  for (int d = 0; d < kDt; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
+  float m = kNothing, l = 0.f;
+
+  // Chunk e of a page's keys is row e / (D / 16), of its values group e / D
+  // and dimension e % D.  Threads without one repeat the last and put it where
+  // its own thread does.
+  const uint32_t base = lds_addr(lds);
+  uint32_t to_k[kChunks][2], to_v[kChunks];
+  int group_v[kChunks], from[kChunks];
+#pragma unroll
+  for (int n = 0; n < kChunks; ++n) {
+    const int e = min(static_cast<int>(threadIdx.x) + kThreads * n, 4 * D - 1), per = D / 16;
+    const int kr = e / per, c = 2 * (e - kr * per), gv = e / D, d = e - gv * D;
+    from[n] = e * 16;
+    group_v[n] = gv;
+    to_k[n][0] = base + kr * (2 * kDims) + ((c ^ (kr & (8 * DC - 1))) << 4);
+    to_k[n][1] = base + kr * (2 * kDims) + (((c + 1) ^ (kr & (8 * DC - 1))) << 4);
+    to_v[n] = base + 2 * kTile + (((d >> 5) * 64 + (gv & 1) * 32 + (d & 31)) << 4) + 8 * (gv >> 1);
+  }
+  // dimensions past D are zeros in every buffer, and stay it
+  if (D < kDims) {
+    for (int e = threadIdx.x; e < 4 * kTile / 16; e += kThreads) reinterpret_cast<v4u*>(lds)[e] = v4u{0, 0, 0, 0};
+    __syncthreads();
+  }
+  const int32_t* const table = a.seq.table + static_cast<int64_t>(t.b) * a.seq.width;
+  // the sequence's pages, 64 at a time, a lane each: asked for in order.  -1: a
+  // page that is not there
+  int ids = 0;
+  auto page_at = [&](int i) {
+    if ((i & 63) == 0) ids = table[min(i + lane, last - 1)];
+    const int page = __builtin_amdgcn_readlane(ids, i & 63);
+    return page < a.seq.pages ? page : -1;
+  };
+  auto slot_of = [&](int page) { return static_cast<int64_t>(max(page, 0)) * a.heads_k + t.h; };
+  v4u raw_k[kChunks], raw_v[kChunks];
+  auto fetch = [&](const uint8_t* cache, int page, v4u (&raw)[kChunks]) {
+    const uint8_t* const p = cache + slot_of(page) * kPage * D;
+#pragma unroll
+    for (int n = 0; n < kChunks; ++n) raw[n] = codes16<false>(p + from[n]);
+  };
+  // what lies past the sequence may hold anything, NaN too
+  auto clean = [&](int key0, int length) {
+    if (key0 + kPage > length)
+#pragma unroll
+      for (int n = 0; n < kChunks; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rest = length - key0 - 16 * i - 4 * group_v[n];
+          raw_v[n][i] &= rest >= 4 ? 0xFFFFFFFFu : rest <= 0 ? 0u : (1u << (8 * rest)) - 1u;
+        }
+  };
+  using Lds16 = __attribute__((address_space(3))) v4u*;
+  using Lds8 = __attribute__((address_space(3))) v2u*;
+  // piece i of 6 of what a thread widens of a chunk: 2 of keys, 4 of values
+  constexpr int kPieces = 6 * kChunks;
+  auto widen_piece = [&](int i, uint32_t off_k, uint32_t off_v) {
+    const int n = i / 6, p = i % 6;
+    if (p < 2) {
+      *reinterpret_cast<Lds16>(to_k[n][p] + off_k) = widen8<E>(raw_k[n][2 * p], raw_k[n][2 * p + 1]);
+    } else {
+      const uint32_t c = raw_v[n][p - 2];
+      *reinterpret_cast<Lds8>(to_v[n] + off_v + (p - 2) * kDt * 1024) = v2u{widen<E>(c, false), widen<E>(c, true)};
+    }
+  };
+  const uint32_t rk = base + l32 * (2 * kDims), rv = base + 2 * kTile + lane * 16;
+  auto read_k = [&](uint32_t off, int kt, int st) {
+    return lds_read16(rk + off + kt * 32 * (2 * kDims) + (((2 * st + h) ^ (l32 & (8 * DC - 1))) << 4));
+  };
+  auto read_v = [&](uint32_t off, int ks, int d) { return lds_read16(rv + off + (ks * kDt + d) * 1024); };
+  struct Exponents {
+    int k, v;
+  };
+  auto exponents = [&](int page) {
+    const int8_t* const e = a.exponents + slot_of(page) * 2;
+    return Exponents{clamp_exponent(e[0]), clamp_exponent(e[1])};
+  };
+  auto mask = [&](v16f (&s)[2], int page, int at) {
+    if (page >= 0 && (at + 1) * kPage <= every) return;
+    const int rest = (page >= 0 ? sees : 0) - at * kPage - 4 * h;
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[kt][e] = kt * 32 + (e >> 2) * 8 + (e & 3) < rest ? s[kt][e] : -INFINITY;
+  };
+  auto pair_max = [](float v) {   // over the two lanes that hold a row's keys
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  };
+  auto length_of = [&](int page) { return page >= 0 ? t.length : 0; };
+
+  if (last > 0) {
+    // pages at, at + 1, at + 2 of the iteration, and the exponents of the first two
+    int id0 = page_at(0);
+    int id1 = page_at(1);
+    int id2 = page_at(2);
+    Exponents x0 = exponents(id0), x1 = exponents(id1);
+    fetch(a.k_cache, id0, raw_k);
+    fetch(a.v_cache, id0, raw_v);
+    clean(0, length_of(id0));
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) widen_piece(i, 0, 0);
+    fetch(a.k_cache, id1, raw_k);
+#pragma unroll
+    for (int n = 0; n < kChunks; ++n)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) widen_piece(6 * n + p, kTile, 0);
+    fetch(a.k_cache, id2, raw_k);
+    fetch(a.v_cache, id1, raw_v);
+    lds_barrier();
+    v16f s0[2], s1[2];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s0[kt][e] = 0.f;
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) s0[kt] = E::mfma(read_k(0, kt, st), q[st], s0[kt]);
+    }
+    mask(s0, id0, 0);
+    float top = s0[0][0];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, s0[kt][e]);
+    top = pair_max(top);
+    lds_barrier();   // K of the first page is read out
+
+    // page at's scores in s, whose maxima are in top; those of the next go to s_next
+    auto iterate = [&](int at, v16f (&s)[2], v16f (&s_next)[2], auto odd) {
+      constexpr uint32_t k_free = decltype(odd)::value ? kTile : 0, v_now = k_free;   // buffers of page at
+      constexpr uint32_t k_next = kTile - k_free, v_free = k_next;
+      const float mul = a.scale * power2(x0.k), add = static_cast<float>(x0.v);
+      top = top * mul + add;
+      if (__ballot(top > m + kSlack)) {
+        const float now = fmaxf(m, top), shrink = exp2_fast(m - now);
+        m = now;
+        l *= shrink;
+#pragma unroll
+        for (int d = 0; d < kDt; ++d) o[d] *= shrink;
+      }
+      clean((at + 1) * kPage, length_of(id1));
+      const float less = add - m;
+      v4u p[4], f[kAhead];
+      float sum[2] = {0.f, 0.f};
+      // pairs of weights that go beside product j of n
+      auto weigh = [&](int first, int count, int j, int n) {
+#pragma unroll
+        for (int i = first + j * count / n; i < first + (j + 1) * count / n; ++i) {
+          const int kt = i >> 3, e = (i & 7) * 2;
+          const float u = exp2_fast(__builtin_fmaf(s[kt][e], mul, less)), v = exp2_fast(__builtin_fmaf(s[kt][e + 1], mul, less));
+          sum[0] += u;
+          sum[1] += v;
+          uint32_t pair = E::pack2(u, v);
+          asm volatile("" : "+v"(pair), "+v"(sum[0]), "+v"(sum[1]));   // here, and not where it is used
+          p[i >> 2][i & 3] = pair;
+        }
+      };
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) f[j] = read_k(k_next, j % 2, j / 2);
+#pragma unroll
+      for (int j = 0; j < kProducts; ++j) {
+        if (j < 2) s_next[j] = v16f{};
+        s_next[j % 2] = E::mfma(f[j % kAhead], q[j / 2], s_next[j % 2]);
+        const int n = j + kAhead;
+        f[j % kAhead] = n < kProducts ? read_k(k_next, n % 2, n / 2) : read_v(v_now, (n - kProducts) / kDt, (n - kProducts) % kDt);
+        weigh(0, kWeights - kLate, j, kProducts);
+        fence();
+      }
+      mask(s_next, id1, at + 1);
+      float high = s_next[0][0];
+      order();
+#pragma unroll
+      for (int j = 0; j < kProducts; ++j) {
+        o[j % kDt] = E::mfma(f[j % kAhead], p[j / kDt], o[j % kDt]);
+        if (j + kAhead < kProducts) f[j % kAhead] = read_v(v_now, (j + kAhead) / kDt, (j + kAhead) % kDt);
+        // the last weights before the products that take them, then the maxima
+        constexpr int kHalf = kProducts / 2, kE = 32 / kHalf;
+        if (j < kHalf) {
+          weigh(kWeights - kLate, kLate, j, kHalf);
+        } else {
+#pragma unroll
+          for (int e = (j - kHalf) * kE; e < (j - kHalf + 1) * kE; ++e) high = fmaxf(high, s_next[e / 16][e % 16]);
+        }
+#pragma unroll
+        for (int i = j * kPieces / kProducts; i < (j + 1) * kPieces / kProducts; ++i) widen_piece(i, k_free, v_free);
+        fence();
+      }
+      l += (sum[0] + sum[1]) * power2(-x0.v);
+      top = pair_max(high);
+      id0 = id1;
+      id1 = id2;
+      id2 = page_at(at + 3);
+      x0 = x1;
+      x1 = exponents(id1);
+      fetch(a.k_cache, id2, raw_k);
+      fetch(a.v_cache, id1, raw_v);
+      // this page's V and the next one's K are read out, what was widened is there; loads stay in flight
+      lds_barrier();
+    };
+    if (idle) {   // rows past the sequence's: the wave widens, and waits for the others
+      for (int at = 0; at < last; ++at) {
+        clean((at + 1) * kPage, length_of(id1));
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) widen_piece(i, (at & 1) * kTile, ((at + 1) & 1) * kTile);
+        id1 = id2;
+        id2 = page_at(at + 3);
+        fetch(a.k_cache, id2, raw_k);
+        fetch(a.v_cache, id1, raw_v);
+        lds_barrier();
+      }
+    } else {
+      for (int at = 0; at < last; at += 2) {
+        iterate(at, s0, s1, std::false_type{});
+        if (at + 1 < last) iterate(at + 1, s1, s0, std::true_type{});
+      }
+    }
+  }
+  if (!valid) return;
+  const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+  const float sum = __uint_as_float(both[0]) + __uint_as_float(both[1]);
+  const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+  if (h == 0) put_lse(a, t, r, m, sum);
+  uint16_t* const to = a.o + (t.start + token) * a.ldo + head * a.hdo + 4 * h;
+#pragma unroll
+  for (int d = 0; d < kDt; ++d)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (d * 32 + 8 * j < D) {
+        const v2u v = {E::pack2(o[d][4 * j] * inv, o[d][4 * j + 1] * inv), E::pack2(o[d][4 * j + 2] * inv, o[d][4 * j + 3] * inv)};
+        __builtin_memcpy(to + d * 32 + 8 * j, &v, 8);
+      }
 }
 
 // Schedules, by sizes alone: rows of a tile, and workgroups that take equal
@@ -534,10 +807,23 @@ struct Plan {
   int rows, groups;
   size_t bytes;
 };
+// Up to 32 rows a sequence a tile has them all.  With more, tiles of many rows
+// read a page once for all of them, but a tile's pages are one workgroup's:
+// few such tiles leave most CUs idle (64 tokens of 32 / 8 heads against 8000
+// keys 231 us), and equal shares of tiles of 32 rows are cheaper.  Estimated in
+// us for a table's width of keys: a page takes a tile of many rows 1.9 with one
+// workgroup a CU, 2.2 with all of them at work, and a share of 32 rows 0.6.
 Plan plan_for(int total, int batch, int width, int heads_q, int heads_k, int D) {
   const int64_t rows = static_cast<int64_t>(total) * (heads_q / heads_k);
-  Plan p{128, 0, 0};
-  if (rows <= 32LL * batch) {
+  const int many = D > 64 ? 256 : 128;
+  bool few = rows <= 32LL * batch;
+  if (!few) {
+    const double tiles_many = static_cast<double>(rows / many + batch) * heads_k / (many == 256 ? kCUs : 2 * kCUs);
+    const double tiles_few = static_cast<double>(rows / 32 + batch) * heads_k / (2 * kCUs);
+    few = tiles_few * (width + kStart) * 0.6 + 12. < (tiles_many < 1. ? 1.9 : 2.2 * tiles_many) * width;
+  }
+  Plan p{many, 0, 0};
+  if (few) {
     p.rows = rows <= 16LL * batch ? 16 : 32;
     // up to 1024 keys a workgroup has them soon; past that every CU takes its share
     if (width > 16) {
@@ -552,8 +838,8 @@ template <typename E, int DC>
 void start(const PagedArgs& a, const Plan& p, hipStream_t stream) {
   const unsigned tiles = static_cast<unsigned>((static_cast<int64_t>(a.seq.total) * a.group / p.rows + a.seq.batch) * a.heads_k);
   const unsigned blocks = a.part ? a.groups : tiles;
-  if (p.rows == 128)
-    k_paged_many<E, DC><<<tiles, 256, 0, stream>>>(a);
+  if (p.rows > 32)
+    k_paged_many<E, DC, 4 * DC><<<tiles, 256 * DC, 0, stream>>>(a);
   else if (p.rows == 16)
     k_paged_few<E, DC, 1><<<blocks, kWaves * 64, 0, stream>>>(a);
   else

@@ -170,6 +170,16 @@ def test_paged_workspace_and_plan():
     assert bq.attention_paged_workspace_size(1, 1, 256, 8, 2, 128) > 0 and bq.attention_paged_workspace_size(1, 1, 4, 8, 2, 128) == 0
 
 
+def test_paged_sizes_reach_every_schedule():
+    from tests import test_gpu_attention_paged as paged
+    for new, lens, hq, hk, d, _ in paged.MANY:
+        width = max(-(-n // bq.PAGE) for n in lens) + 2
+        assert paged.plan(sum(new), len(new), width, hq, hk, d) == (256 if d > 64 else 128, 0), (new, lens)
+    for args, want in (((8, 8, 30, 8, 2, 128), (16, 512)), ((8, 8, 16, 8, 2, 128), (16, 0)), ((40, 8, 30, 8, 2, 128), (32, 512)),
+                       ((40, 8, 10, 8, 2, 128), (32, 0)), ((64, 1, 128, 32, 8, 128), (32, 512)), ((3050, 4, 127, 32, 8, 128), (256, 0))):
+        assert paged.plan(*args) == want, args
+
+
 @pytest.mark.skipif(_gpu_present(), reason="checks the no-device path")
 def test_no_device_cache():
     assert _call(bq.lib.svdq_cache_append, APPEND, {}) == bq.SVDQ_ERR_UNSUPPORTED_DEVICE

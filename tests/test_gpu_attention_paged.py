@@ -84,6 +84,60 @@ def test_chunks(causal):
         check([64, 64], [64, 1000], 6, 6, d, dtype, causal=causal)
 
 
+# sizes that tiles of many rows take: (new, lens, heads_q, heads_k, head_dim, causal)
+MANY = [
+    ([700, 300], [1290, 365], 32, 8, 128, True), ([700, 300], [1300, 300], 32, 8, 128, False), ([1000], [1000], 32, 8, 64, True),
+    ([1100, 129], [1281, 129], 32, 8, 80, True), ([913, 400], [912, 1000], 32, 8, 112, False), ([900, 77], [960, 78], 32, 8, 48, True),
+    ([600, 1, 5, 0, 8, 300], [700, 1200, 5, 70, 64, 1], 32, 8, 128, True),      # single tokens, and more queries than keys, among them
+    ([700, 400], [700, 449], 32, 16, 96, True), ([1030], [1030], 32, 8, 16, True),
+]
+
+
+@pytest.mark.parametrize("case", MANY)
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_many_rows(case, dtype):
+    new, lens, hq, hk, d, causal = case
+    check(new, lens, hq, hk, d, dtype, causal=causal)
+
+
+def test_many_rows_exponents_and_scores():
+    for low, high, scale in ((-40, 40, 2.0 ** -51), (20, 40, 2.0 ** -51), (-6, 0, 0.5), (-6, 0, 2.0 ** -20)):
+        check([700, 300], [1290, 365], 32, 8, 128, BF, low=low, high=high, scale=scale)
+        check([1000], [1000], 32, 8, 64, HF, low=low, high=high, scale=scale)
+
+
+def test_many_rows_of_pages_that_are_not_there():
+    g = torch.Generator().manual_seed(14)
+    for d in (64, 128):
+        cache = random_cache(24, 8, d, g)
+        cache.k.view(torch.uint8)[0], cache.v.view(torch.uint8)[0] = 0x7F, 0x7F       # page 0 is nobody's
+        table = torch.arange(1, 24, dtype=torch.int32).repeat(2)[:40].view(2, 20).cuda()
+        table[0, 3], table[0, 19], table[1, 0], table[1, 7] = -1, 24, -(2 ** 31), 2 ** 31 - 1
+        new, lens = [900, 150], [1250, 700]
+        assert plan(1070, 2, 20, 32, 8, d)[0] > 32
+        q = torch.randn(1070, 32, d, generator=g).to(BF).cuda()
+        o, lse = bq.attention_paged(q, cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), cu_seqlens_q=starts(new) + 7,
+                                    scale=2.0 ** -12, return_lse=True)
+        want, want_lse, bound, bound_lse = paged_reference(q, cache, table, torch.tensor(lens), new, True, 2.0 ** -12, first=7)
+        assert_within(o, want, bound, "o")
+        assert_within(lse, want_lse, bound_lse, "lse")
+        assert (o[:7] == 0).all() and (o[-13:] == 0).all() and (lse[:7] == -math.inf).all() and (lse[-13:] == -math.inf).all()
+        for cu in ([0, 5000, -3], [-5, 10, 5], [0, 999, 0]):
+            for lengths in ([-1, 2 ** 31 - 1], [0, 0], [2 ** 31 - 1, -2 ** 31]):
+                bq.attention_paged(q, cache, table, torch.tensor(lengths, dtype=torch.int32, device="cuda"),
+                                   cu_seqlens_q=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+        torch.cuda.synchronize()
+
+
+def test_chunks_against_long_caches():
+    # more than 32 rows a sequence, few tiles: equal shares of tiles of 32 rows
+    for new, lens, hq, hk, d in (([40], [3000], 8, 2, 128), ([64, 20, 1], [2000, 20, 1500], 4, 2, 64)):
+        assert plan(sum(new), len(new), max(-(-n // PAGE) for n in lens) + 2, hq, hk, d) == (32, 512)
+        check(new, lens, hq, hk, d, BF)
+        check(new, lens, hq, hk, d, HF, causal=False)
+        check(new, lens, hq, hk, d, BF, workspace=None)
+
+
 def test_shares():
     """Long caches of very different lengths, cut into equal shares, and without a workspace."""
     lens = [5000, 3, 0, 1, 2000, 64, 1900, 129]
