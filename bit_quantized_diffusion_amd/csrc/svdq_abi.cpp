@@ -80,9 +80,9 @@ int check_codes(int K) { return K < 16 || K % 16 || K > 1 << 22 ? SVDQ_ERR_SHAPE
 
 int check_gemm_fp8_shape(int M, int N, int K) {
   if (M < 1 || N < 1 || M > kMostRows || N > (1 << 28) - 32) return SVDQ_ERR_SHAPE;
-  // a launch holds less than 2^32 threads: 256 for a tile of 64 x 64 or more,
-  // or for 16 channels of few rows
-  if (((M + 63LL) / 64) * ((N + 63LL) / 64) >= 1LL << 24) return SVDQ_ERR_SHAPE;
+  // a launch holds less than 2^32 threads: at most 512 for a tile of 64 rows
+  // and up to 64 channels, or for 32 channels of few rows
+  if (((M + 63LL) / 64) * ((N + 63LL) / 64) >= 1LL << 23) return SVDQ_ERR_SHAPE;
   return check_codes(K);
 }
 
@@ -540,7 +540,7 @@ int svdq_attention_paged(const void* q, void* o, float* lse, const int64_t* stri
       !aligned4(lse) || !aligned4(block_table) || !aligned4(lengths) || !aligned4(cu_seqlens))
     return SVDQ_ERR_INVALID_ARG;
   if (!strides_fit(strides, 4, 8)) return SVDQ_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || std::isinf(scale * 2.f)) return SVDQ_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !(scale < 0x1p80f)) return SVDQ_ERR_INVALID_ARG;   // a page's exponent goes with it
   if ((st = current_device_ok())) return st;
   if (total == 0) return SVDQ_OK;
   return hip_status(svdq_launch_attention_paged(q, o, lse, strides, k_cache, v_cache, exponents, pages, block_table,

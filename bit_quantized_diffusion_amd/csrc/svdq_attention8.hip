@@ -81,15 +81,12 @@ __device__ __forceinline__ int visible(const PagedArgs& a, const Tile& t, int r)
   return a.causal ? max(0, min(t.length, t.length - t.tokens + row / a.group + 1)) : t.length;
 }
 
-// 16 RT rows against pages: DC chunks of 64 dimensions.  Codes that no other
-// workgroup reads bypass the caches' keeping (ONCE; 64 caches of 3000 to 5300
-// tokens 111 -> 99 us).
-template <bool ONCE>
-__device__ __forceinline__ v4u codes16(const uint8_t* p) {
-  const v4u* const v = reinterpret_cast<const v4u*>(p);
-  return ONCE ? __builtin_nontemporal_load(v) : *v;
-}
-template <typename E, int DC, int RT, bool ONCE>
+// 16 codes that few workgroups read: past the caches' keeping (64 caches of
+// 3000 to 5300 tokens 111 -> 99 us)
+__device__ __forceinline__ v4u stream16(const uint8_t* p) { return __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p)); }
+
+// 16 RT rows against pages: DC chunks of 64 dimensions.
+template <typename E, int DC, int RT>
 struct Rows {
   v4u q[RT][DC][2];
   v4u k[4][DC], v[4 * DC];    // a page's codes as they lie
@@ -132,7 +129,7 @@ struct Rows {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int c = 0; c < DC; ++c)
-        k[i][c] = 64 * c + 16 * g < D ? codes16<ONCE>(p + i * 16 * D + 64 * c) : v4u{0, 0, 0, 0};
+        k[i][c] = 64 * c + 16 * g < D ? stream16(p + i * 16 * D + 64 * c) : v4u{0, 0, 0, 0};
     ek = a.exponents[slot * 2];
     ev = a.exponents[slot * 2 + 1];
   }
@@ -142,7 +139,7 @@ struct Rows {
     const uint8_t* const p = a.v_cache + slot * kPage * D + (g * D + l16) * 16;
 #pragma unroll
     for (int d = 0; d < 4 * DC; ++d)
-      v[d] = d * 16 < D ? codes16<ONCE>(p + d * 256) : v4u{0, 0, 0, 0};
+      v[d] = d * 16 < D ? stream16(p + d * 256) : v4u{0, 0, 0, 0};
   }
 
   // Pages first, first + step, ... before last; up to key `all_see` every row
@@ -348,7 +345,7 @@ __device__ __forceinline__ void few_rows(const PagedArgs& a, const Tile& t, int 
   constexpr int kRows = 16 * RT;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), D = a.head_dim;
   const int rows = min(kRows, t.tokens * a.group - t.row0);
-  Rows<E, DC, RT, true> r;
+  Rows<E, DC, RT> r;
   r.init(a, t, 0);
   r.walk(a, t, first + wave, last, NW, visible(a, t, 0));
   // the waves' parts, joined in their order
@@ -607,7 +604,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_paged_many(PagedArgs a) {
   auto fetch = [&](const uint8_t* cache, int page, v4u (&raw)[kChunks]) {
     const uint8_t* const p = cache + slot_of(page) * kPage * D;
 #pragma unroll
-    for (int n = 0; n < kChunks; ++n) raw[n] = codes16<false>(p + from[n]);
+    for (int n = 0; n < kChunks; ++n) raw[n] = *reinterpret_cast<const v4u*>(p + from[n]);
   };
   // what lies past the sequence may hold anything, NaN too
   auto clean = [&](int key0, int length) {

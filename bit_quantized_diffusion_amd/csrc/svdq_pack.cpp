@@ -17,6 +17,7 @@
 #include <cstring>
 #include <functional>
 #include <random>
+#include <system_error>
 #include <thread>
 #include <vector>
 
@@ -155,7 +156,11 @@ void parallel_for(int64_t n, const std::function<void(int64_t)>& body, int64_t c
   };
   std::vector<std::thread> pool;
   pool.reserve(nt - 1);
-  for (int t = 0; t < nt - 1; ++t) pool.emplace_back(worker);
+  // a thread that cannot be had leaves its work to the others
+  try {
+    for (int t = 0; t < nt - 1; ++t) pool.emplace_back(worker);
+  } catch (const std::system_error&) {
+  }
   worker();
   for (auto& th : pool) th.join();
 }

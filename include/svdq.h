@@ -489,7 +489,7 @@ SVDQ_API int svdq_pack_fp8(const uint16_t* w, int K, int N, int dtype, uint8_t* 
  * products of 8 consecutive k to the largest one's exponent E and cuts what
  * lies below 2^(E - 13) (about 1e-4 of a result of 4096 products); y is
  * rounded once and overlaps no operand but residual.
- * M, N >= 1, M at most 2^31 - 2^16, N at most 2^28 - 32, fewer than 2^24 tiles
+ * M, N >= 1, M at most 2^31 - 2^16, N at most 2^28 - 32, fewer than 2^23 tiles
  * of 64 x 64 in the result; K a multiple of 16 to 2^22.
  * Results are deterministic. */
 SVDQ_API int svdq_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const void* bias,
@@ -552,7 +552,7 @@ SVDQ_API int svdq_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq
  * places past a sequence's length may hold anything; a NaN at a key that only
  * causal masking hides can reach a query.  The codes are taken exactly; P is
  * rounded to 16 bits for the matrix core; softmax statistics and sums are
- * fp32.  o overlaps no operand.  0 < scale < 2^127.
+ * fp32.  o overlaps no operand.  0 < scale < 2^80.
  * workspace (dev, 16-byte aligned): with the bytes that
  * svdq_attention_paged_workspace_size names, calls with few queries a sequence
  * cut the keys into equal shares, which a second kernel joins in a fixed

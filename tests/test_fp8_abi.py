@@ -57,7 +57,7 @@ def test_quantize_refuses(kw, want):
     (dict(act=3), BAD), (dict(dtype=-1), BAD), (dict(m=0), SHAPE), (dict(n=0), SHAPE), (dict(k=0), SHAPE), (dict(k=72), SHAPE),
     (dict(k=(1 << 22) + 16), SHAPE), (dict(ldy=31), SHAPE), (dict(ldr=31), SHAPE), (dict(ld_gate=31), SHAPE), (dict(rows=0), SHAPE),
     (dict(m=2 ** 31 - 100), SHAPE), (dict(n=2 ** 28, ldy=2 ** 28, ldr=2 ** 28, ld_gate=2 ** 28), SHAPE),
-    (dict(m=2 ** 29, n=128, ldy=128, ldr=128, ld_gate=128), SHAPE),
+    (dict(m=2 ** 28, n=128, ldy=128, ldr=128, ld_gate=128), SHAPE), (dict(m=2 ** 29, n=16, ldy=16, ldr=16, ld_gate=16), SHAPE),
 ])
 def test_gemm_refuses(kw, want):
     assert bq.lib.svdq_gemm_fp8(*dict(GEMM, **kw).values(), None) == want
@@ -156,7 +156,7 @@ def test_append_refuses(kw, want):
 
 @pytest.mark.parametrize("kw,want", SHAPES + [
     (dict(q=None), BAD), (dict(o=None), BAD), (dict(q=OFF), BAD), (dict(o=OFF), BAD), (dict(lse=ODD), BAD), (dict(ws=OFF), BAD), (dict(scale=0.0), BAD),
-    (dict(scale=math.nan), BAD), (dict(scale=3e38), BAD), (dict(strides=(256, 60, 256, 64)), BAD), (dict(strides=(256, 64, -256, 64)), BAD),
+    (dict(scale=math.nan), BAD), (dict(scale=2.0 ** 80), BAD), (dict(strides=(256, 60, 256, 64)), BAD), (dict(strides=(256, 64, -256, 64)), BAD),
 ])
 def test_attention_paged_refuses(kw, want):
     assert _call(bq.lib.svdq_attention_paged, PAGED, kw) == want

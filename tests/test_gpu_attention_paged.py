@@ -89,7 +89,7 @@ MANY = [
     ([700, 300], [1290, 365], 32, 8, 128, True), ([700, 300], [1300, 300], 32, 8, 128, False), ([1000], [1000], 32, 8, 64, True),
     ([1100, 129], [1281, 129], 32, 8, 80, True), ([913, 400], [912, 1000], 32, 8, 112, False), ([900, 77], [960, 78], 32, 8, 48, True),
     ([600, 1, 5, 0, 8, 300], [700, 1200, 5, 70, 64, 1], 32, 8, 128, True),      # single tokens, and more queries than keys, among them
-    ([700, 400], [700, 449], 32, 16, 96, True), ([1030], [1030], 32, 8, 16, True),
+    ([600, 1, 5, 0, 8, 300], [700, 1000, 5, 70, 64, 1], 32, 8, 64, True), ([700, 400], [700, 449], 32, 16, 96, True), ([1030], [1030], 32, 8, 16, True),
 ]
 
 
