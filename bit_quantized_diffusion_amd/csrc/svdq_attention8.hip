@@ -71,14 +71,15 @@ __device__ __forceinline__ v4u widen8(uint32_t lo, uint32_t hi) {
 // A tile: the sequence's rows from row0 on, of one key head.
 struct Tile {
   int b, h, row0;
-  int tokens, length, start;   // the sequence's
+  int tokens, length, start;   // the sequence's, its keys as far as the table holds them
+  int before;                  // its keys before the first of the tokens, also those past the table; below 0 if there are more tokens
 };
 
 // Keys that row r of a tile sees.
 __device__ __forceinline__ int visible(const PagedArgs& a, const Tile& t, int r) {
   const int row = t.row0 + r;
   if (row >= t.tokens * a.group) return 0;
-  return a.causal ? max(0, min(t.length, t.length - t.tokens + row / a.group + 1)) : t.length;
+  return a.causal ? max(0, min(t.length, t.before + row / a.group + 1)) : t.length;
 }
 
 // 16 codes that few workgroups read: past the caches' keeping (64 caches of
@@ -313,6 +314,7 @@ __device__ __forceinline__ Tile tile_at(const PagedArgs& a, int b, int x, int ro
   t.tokens = __builtin_amdgcn_readfirstlane(a.seq.tokens(b));
   t.length = __builtin_amdgcn_readfirstlane(a.seq.length(b));
   t.start = __builtin_amdgcn_readfirstlane(a.seq.start(b));
+  t.before = __builtin_amdgcn_readfirstlane(max(a.seq.lengths[b], 0)) - t.tokens;
   return t;
 }
 

@@ -151,7 +151,7 @@ def paged_reference(q, cache, table, lengths, new, causal, scale, first=0):
         page = torch.where(there, page, 0)
         hidden = torch.zeros(n, length, dtype=torch.bool) | ~there[None, :]
         if causal:
-            hidden |= at[None, :] > torch.arange(n)[:, None] + (length - n)
+            hidden |= at[None, :] > torch.arange(n)[:, None] + (max(int(lengths[b]), 0) - n)
         for h in range(hq if length and n else 0):
             g = h * hk // hq
             power = torch.exp2(e[page, g])                                        # [keys][2]

@@ -218,6 +218,14 @@ def test_hidden_rows():
         check(new, lens, 4, 2, 64, BF)
 
 
+def test_lengths_past_the_table():
+    # keys past the table are hidden; the tokens stand where the length says
+    for new, lens, width in (([1, 1], [150, 129], 2), ([4, 2], [130, 128], 2), ([5], [1400], 21), ([100], [230], 3), ([40, 90], [150, 300], 3),
+                             ([300], [500], 5)):
+        check(new, lens, 4, 2, 64, BF, width=width)
+        check(new, lens, 4, 2, 128, HF, width=width)
+
+
 def test_far_pages():
     pages = 2 ** 31 // (2 * PAGE * 128) + 5
     cache = bq.KVCache.allocate(pages, 2, 128)
