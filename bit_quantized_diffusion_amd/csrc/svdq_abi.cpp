@@ -87,14 +87,15 @@ int check_gemm_fp8_shape(int M, int N, int K) {
 }
 
 int check_paged_shape(int total, int batch, int width, int heads_q, int heads_k, int head_dim) {
-  if (total < 0 || batch < 1 || width < 1 || heads_q < 1 || heads_k < 1 || heads_q % heads_k) return SVDQ_ERR_SHAPE;
+  if (total < 0 || batch < 1 || width < 1 || width > 1 << 24 || heads_q < 1 || heads_k < 1 || heads_q % heads_k) return SVDQ_ERR_SHAPE;
   if (head_dim < 16 || head_dim > 128 || head_dim % 16) return SVDQ_ERR_SHAPE;
-  // pages of all tiles of 16 rows are counted in 31 bits; a launch holds less
+  // positions, and pages of all tiles of 16 rows with 4 for each one's start,
+  // are counted in 31 bits; a launch holds less
   // than 2^32 threads: 256 for such a tile, for a touched page of a head, or
   // for a token's queries
   const long long rows = static_cast<long long>(total) * (heads_q / heads_k), hk = heads_k;
   if (rows > kMostRows || rows / 16 + 2LL * batch + total >= (1LL << 24) / hk) return SVDQ_ERR_SHAPE;
-  if ((rows / 16 + batch) * hk >= (1LL << 31) / width) return SVDQ_ERR_SHAPE;
+  if ((rows / 16 + batch) * hk >= (1LL << 31) / (width + 4)) return SVDQ_ERR_SHAPE;
   return SVDQ_OK;
 }
 
@@ -540,7 +541,7 @@ int svdq_attention_paged(const void* q, void* o, float* lse, const int64_t* stri
       !aligned4(lse) || !aligned4(block_table) || !aligned4(lengths) || !aligned4(cu_seqlens))
     return SVDQ_ERR_INVALID_ARG;
   if (!strides_fit(strides, 4, 8)) return SVDQ_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !(scale < 0x1p80f)) return SVDQ_ERR_INVALID_ARG;   // a page's exponent goes with it
+  if (!(scale >= 0x1p-80f) || !(scale < 0x1p80f)) return SVDQ_ERR_INVALID_ARG;   // a page's exponent goes with it
   if ((st = current_device_ok())) return st;
   if (total == 0) return SVDQ_OK;
   return hip_status(svdq_launch_attention_paged(q, o, lse, strides, k_cache, v_cache, exponents, pages, block_table,

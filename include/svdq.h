@@ -552,7 +552,7 @@ SVDQ_API int svdq_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq
  * places past a sequence's length may hold anything; a NaN at a key that only
  * causal masking hides can reach a query.  The codes are taken exactly; P is
  * rounded to 16 bits for the matrix core; softmax statistics and sums are
- * fp32.  o overlaps no operand.  0 < scale < 2^80.
+ * fp32.  o overlaps no operand.  2^-80 <= scale < 2^80.
  * workspace (dev, 16-byte aligned): with the bytes that
  * svdq_attention_paged_workspace_size names, calls with few queries a sequence
  * cut the keys into equal shares, which a second kernel joins in a fixed
@@ -560,9 +560,9 @@ SVDQ_API int svdq_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq
  * queries.  Results are deterministic; the schedule goes by sizes alone.
  *
  * Both: head_dim a multiple of 16 from 16 to 128; heads_q a multiple of
- * heads_k; batch, pages, table_width >= 1; total >= 0; caches 16-byte
- * aligned; (total (heads_q / heads_k) / 16 + batch) heads_k table_width below
- * 2^31, and (total (heads_q / heads_k) / 16 + 2 batch + total) heads_k below 2^24. */
+ * heads_k; batch, pages >= 1; table_width from 1 to 2^24; total >= 0; caches
+ * 16-byte aligned; (total (heads_q / heads_k) / 16 + batch) heads_k
+ * (table_width + 4) below 2^31, and (total (heads_q / heads_k) / 16 + 2 batch + total) heads_k below 2^24. */
 #define SVDQ_PAGE 64
 SVDQ_API int svdq_cache_append(const void* q, const void* k, const void* v, void* q_out, const int64_t* strides,
                               uint8_t* k_cache, uint8_t* v_cache, int8_t* exponents, int pages,

@@ -139,7 +139,7 @@ def _call(fn, defaults, kw):
 SHAPES = [
     (dict(batch=0), SHAPE), (dict(total=-1), SHAPE), (dict(width=0), SHAPE), (dict(hq=0), SHAPE), (dict(hk=0), SHAPE), (dict(hk=3), SHAPE),
     (dict(pages=0), SHAPE), (dict(d=8), SHAPE), (dict(d=72), SHAPE), (dict(d=144), SHAPE), (dict(cu=None), SHAPE), (dict(total=2 ** 24), SHAPE),
-    (dict(batch=2 ** 23), SHAPE), (dict(width=2 ** 30), SHAPE), (dict(total=2 ** 23, hq=512), SHAPE),
+    (dict(batch=2 ** 23), SHAPE), (dict(width=2 ** 30), SHAPE), (dict(width=2 ** 24 + 1, hq=1, hk=1, batch=1, total=1), SHAPE), (dict(total=2 ** 23, hq=512), SHAPE),
     (dict(k8=None), BAD), (dict(v8=None), BAD), (dict(e=None), BAD), (dict(table=None), BAD), (dict(lengths=None), BAD), (dict(strides=None), BAD),
     (dict(k8=OFF), BAD), (dict(v8=OFF), BAD), (dict(table=ODD), BAD), (dict(lengths=ODD), BAD), (dict(cu=ODD), BAD), (dict(dtype=2), BAD),
 ]
@@ -156,7 +156,7 @@ def test_append_refuses(kw, want):
 
 @pytest.mark.parametrize("kw,want", SHAPES + [
     (dict(q=None), BAD), (dict(o=None), BAD), (dict(q=OFF), BAD), (dict(o=OFF), BAD), (dict(lse=ODD), BAD), (dict(ws=OFF), BAD), (dict(scale=0.0), BAD),
-    (dict(scale=math.nan), BAD), (dict(scale=2.0 ** 80), BAD), (dict(strides=(256, 60, 256, 64)), BAD), (dict(strides=(256, 64, -256, 64)), BAD),
+    (dict(scale=math.nan), BAD), (dict(scale=2.0 ** 80), BAD), (dict(scale=2.0 ** -81), BAD), (dict(strides=(256, 60, 256, 64)), BAD), (dict(strides=(256, 64, -256, 64)), BAD),
 ])
 def test_attention_paged_refuses(kw, want):
     assert _call(bq.lib.svdq_attention_paged, PAGED, kw) == want
