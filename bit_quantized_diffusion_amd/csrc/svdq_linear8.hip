@@ -16,6 +16,11 @@
 // are added in fp32.  For random codes that is about 1e-4 of the result, a
 // sixteenth of a rounding to bf16 and half of one to fp16.  Codes widened to
 // bf16 would be summed exactly, at half the rate.
+//
+// Measured, rows x k x channels: 8 x 4096 x 6144 7.4 us (25 MB of W, 3.4 TB/s), 333 x 4096 x 1536
+// 10.2, 4608 x 4096 x 12288 with GELU 229 (2.0 PFLOP/s), 4608 x 12288 x 4096
+// 212 (2.2 PFLOP/s).  Bound by the power limit, and by the scales' FMAs beside
+// the products: without them the large tiles take 17 % less.
 
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -511,7 +516,7 @@ constexpr int kFewRows = 32;   // up to these the tiles' height goes by the rows
 // The cheapest shape.  Past one round of workgroups the cost lies nearer to
 // the rounded-up than to the true number of rounds: idle CUs of the last one
 // leave the others a higher clock.  The many heights of large tiles are there
-// for that last round: 4608 x 4096 x 12288 takes 16 x 16 tiles of 288 x 256,
+// for that last round: 4608 x 12288 x 4096 takes 16 x 16 tiles of 288 x 256,
 // one round of 205 us, where 18 x 16 of 256 x 256 take two, 295.
 int shape_for(int M, int N, int K) {
   const int stages = (K + 127) / 128;
