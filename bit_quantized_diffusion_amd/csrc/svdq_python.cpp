@@ -489,16 +489,15 @@ PyObject* layer_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return out.release();
 }
 
-// A contiguous tensor of this dtype, shape and device.
-bool exactly(PyObject* o, PyObject* dtype, long device, int dims, int64_t a, int64_t b, int64_t c, const char* name, Tensor& t) {
-  if (!read(o, t)) return no_tensor(name, "");
+// t, read from o, is a contiguous matrix of this dtype, shape and device.
+bool exactly(PyObject* o, const Tensor& t, PyObject* dtype, long device, int64_t a, int64_t b, const char* name) {
   if (t.dtype != dtype || t.device != device || device < 0) {
     PyErr_Format(PyExc_TypeError, "%s: expected %S on cuda:%ld, got %S on device %ld", name, dtype, device, t.dtype, t.device);
     return false;
   }
-  if (!shaped(o, t, dims, a, b, c, name)) return false;
+  if (!shaped(o, t, 2, a, b, 0, name)) return false;
   int64_t dense = 1;
-  for (int i = dims - 1; i >= 0; --i) {
+  for (int i = 1; i >= 0; --i) {
     if (t.shape[i] > 1 && t.stride[i] != dense) {
       PyErr_Format(PyExc_ValueError, "%s: must be contiguous", name);
       return false;
@@ -620,11 +619,14 @@ PyObject* gemm_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
   const int64_t N = wq.shape[0];
   if (!countable({M, N, K}, "gemm_fp8")) return nullptr;
-  if (!whole && (!exactly(args[0], g_f8, x.device, 2, M, K, 0, "xq", x) ||
-                 !exactly(args[1], g_f32, x.device, 2, blocks_of(K), M, 0, "xs", xs)))
+  if ((!whole && !read(args[1], xs)) || !read(args[3], ws)) {
+    no_tensor(whole || xs.dtype ? "ws" : "xs", "");
     return nullptr;
-  if (!exactly(args[2], g_f8, x.device, 2, N, K, 0, "wq", wq) ||
-      !exactly(args[3], g_f32, x.device, 2, blocks_of(N), blocks_of(K), 0, "ws", ws))
+  }
+  if (!whole && (!exactly(args[0], x, g_f8, x.device, M, K, "xq") || !exactly(args[1], xs, g_f32, x.device, blocks_of(K), M, "xs")))
+    return nullptr;
+  if (!exactly(args[2], wq, g_f8, x.device, N, K, "wq") ||
+      !exactly(args[3], ws, g_f32, x.device, blocks_of(N), blocks_of(K), "ws"))
     return nullptr;
   like_y.dtype = code == SVDQ_BF16 ? g_bf16 : g_f16;
   like_y.device = x.device;
@@ -754,7 +756,7 @@ PyObject* cache_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     }
     rope_rows = rope.shape[0];
     rotary = rope.shape[1];
-    if (!exactly(args[9], g_f32, k.device, 2, rope_rows, rotary, 0, "rope", rope)) return nullptr;
+    if (!exactly(args[9], rope, g_f32, k.device, rope_rows, rotary, "rope")) return nullptr;
   }
   const int interleaved = PyObject_IsTrue(args[10]);
   if (interleaved < 0) return nullptr;
