@@ -14,7 +14,7 @@
 // the values, so that no byte has two writers.  Other workgroups take a
 // token's query heads each.
 //
-// Measured: a token of each of 64 sequences, 32 / 8 heads of 128, 8.5 us a
+// Measured: a token of each of 64 sequences, 32 / 8 heads of 128, 8.2 us a
 // call, the host's time for it (one that loads all it can at once takes as
 // long, and prompts 4 % longer); prompts of 141 MB in all 28.8 us by itself,
 // 4.9 TB/s, the rate of a copy.

@@ -17,7 +17,7 @@
 // sixteenth of a rounding to bf16 and half of one to fp16.  Codes widened to
 // bf16 would be summed exactly, at half the rate.
 //
-// Measured, rows x k x channels: 8 x 4096 x 6144 7.4 us (25 MB of W, 3.4 TB/s), 333 x 4096 x 1536
+// Measured, rows x k x channels: 8 x 4096 x 6144 7.2 us (25 MB of W, 3.5 TB/s), 333 x 4096 x 1536
 // 10.2, 4608 x 4096 x 12288 with GELU 229 (2.0 PFLOP/s), 4608 x 12288 x 4096
 // 212 (2.2 PFLOP/s).  Bound by the power limit, and by the scales' FMAs beside
 // the products: without them the large tiles take 17 % less.
