@@ -258,7 +258,10 @@ __device__ __forceinline__ void put(const PagedArgs& a, const Tile& t, int r, in
   const int row = t.row0 + r, token = row / a.group, head = t.h * a.group + row - token * a.group;
   store8(a.o + (t.start + token) * a.ldo + head * a.hdo + d, pack8<E>(f), 8);
 }
-__device__ __forceinline__ float logarithm(float m, float l) { return l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY; }
+// Whether a row with the sum l saw a key.  One that saw none gets zeros, not
+// its sums times zero: the values it weighed with zero may be NaN.
+__device__ __forceinline__ bool saw(float l) { return l > 0.f || l != l; }
+__device__ __forceinline__ float logarithm(float m, float l) { return saw(l) ? (m + log2f(l)) * kLn2 : -INFINITY; }
 __device__ __forceinline__ void put_lse(const PagedArgs& a, const Tile& t, int r, float m, float l) {
   if (!a.lse) return;
   const int row = t.row0 + r, token = row / a.group, head = t.h * a.group + row - token * a.group;
@@ -384,9 +387,9 @@ __device__ __forceinline__ void few_rows(const PagedArgs& a, const Tile& t, int 
       for (int c = 0; c < 8; ++c) f[c] += s * lds.o[w][row][d + c];
     }
     if (!part) {
-      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      const float inv = 1.f / l;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) f[c] *= inv;
+      for (int c = 0; c < 8; ++c) f[c] = saw(l) ? f[c] * inv : 0.f;
       put<E>(a, t, row, d, f);
       if (d == 0) put_lse(a, t, row, top, l);
     } else {
@@ -495,10 +498,10 @@ __global__ __launch_bounds__(256) void k_paged_join(PagedArgs a) {
 #pragma unroll 8
       for (int i = i0 ? 0 : kAhead; i < n; ++i) add(i, values(i0 + i));
     }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const float inv = 1.f / l;
     const int all = note.row0 + row, token = all / a.group, head = note.h * a.group + all - token * a.group;
     if (2 * lane < D) {
-      const uint32_t v = E::pack2(f[0] * inv, f[1] * inv);
+      const uint32_t v = saw(l) ? E::pack2(f[0] * inv, f[1] * inv) : 0u;
       __builtin_memcpy(a.o + (note.start + token) * a.ldo + head * a.hdo + d, &v, 4);
     }
     if (lane == 0 && a.lse)
@@ -792,7 +795,8 @@ __global__ __launch_bounds__(NW * 64, 2) void k_paged_many(PagedArgs a) {
   if (!valid) return;
   const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
   const float sum = __uint_as_float(both[0]) + __uint_as_float(both[1]);
-  const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+  const float inv = 1.f / sum;
+  const bool any = saw(sum);
   if (h == 0) put_lse(a, t, r, m, sum);
   uint16_t* const to = a.o + (t.start + token) * a.ldo + head * a.hdo + 4 * h;
 #pragma unroll
@@ -800,7 +804,8 @@ __global__ __launch_bounds__(NW * 64, 2) void k_paged_many(PagedArgs a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (d * 32 + 8 * j < D) {
-        const v2u v = {E::pack2(o[d][4 * j] * inv, o[d][4 * j + 1] * inv), E::pack2(o[d][4 * j + 2] * inv, o[d][4 * j + 3] * inv)};
+        const v2u v = any ? v2u{E::pack2(o[d][4 * j] * inv, o[d][4 * j + 1] * inv), E::pack2(o[d][4 * j + 2] * inv, o[d][4 * j + 3] * inv)}
+                          : v2u{0, 0};
         __builtin_memcpy(to + d * 32 + 8 * j, &v, 8);
       }
 }

@@ -548,11 +548,12 @@ SVDQ_API int svdq_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq
  *             multiples of 8, not negative
  * Query head h reads key head h / (heads_q / heads_k).  causal != 0: query i of
  * n sees keys j <= i + length - n, else all of its sequence's.  A query that
- * sees no key, or belongs to no sequence, gives o = 0 and lse = -inf.  Pages'
- * places past a sequence's length may hold anything; a NaN at a key that only
- * causal masking hides can reach a query.  The codes are taken exactly; P is
- * rounded to 16 bits for the matrix core; softmax statistics and sums are
- * fp32.  o overlaps no operand.  2^-80 <= scale < 2^80.
+ * sees no key, or belongs to no sequence, gives o = 0 and lse = -inf, whatever
+ * the pages hold.  Pages' places past a sequence's length may hold anything;
+ * a NaN at a key that only causal masking hides can reach a query that sees
+ * others.  The codes are taken exactly; P is rounded to 16 bits for the matrix
+ * core; softmax statistics and sums are fp32.  o overlaps no operand.
+ * 2^-80 <= scale < 2^80.
  * workspace (dev, 16-byte aligned): with the bytes that
  * svdq_attention_paged_workspace_size names, calls with few queries a sequence
  * cut the keys into equal shares, which a second kernel joins in a fixed
