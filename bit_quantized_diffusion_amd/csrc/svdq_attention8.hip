@@ -537,7 +537,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_paged_many(PagedArgs a) {
   constexpr int kRows = NW * 32, kThreads = NW * 64, kDims = 64 * DC, kTile = kPage * kDims * 2;
   constexpr int kChunks = kPage * kDims / 16 / kThreads;   // of 16 codes, a thread's
   constexpr int kSteps = kDims / 16, kDt = kDims / 32, kProducts = 2 * kSteps, kAhead = 4, kWeights = 16, kLate = 4;
-  constexpr float kSlack = 8.f;
+  constexpr float kSlack = 8.f, kFar = 0x1p20f;
   static_assert(kChunks >= 1 && kProducts == 4 * kDt, "work divides evenly");
   using Few = Joined<DC, 1, NW>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[sizeof(Few) > 4 * kTile ? sizeof(Few) : 4 * kTile];   // K, K, V, V
@@ -706,8 +706,9 @@ __global__ __launch_bounds__(NW * 64, 2) void k_paged_many(PagedArgs a) {
     auto iterate = [&](int at, v16f (&s)[2], v16f (&s_next)[2], auto odd) {
       constexpr uint32_t k_free = decltype(odd)::value ? kTile : 0, v_now = k_free;   // buffers of page at
       constexpr uint32_t k_next = kTile - k_free, v_free = k_next;
-      const float mul = a.scale * power2(x0.k), add = static_cast<float>(x0.v);
-      top = top * mul + add;
+      float mul = a.scale * power2(x0.k);
+      const float add = static_cast<float>(x0.v);
+      top = __builtin_fmaf(top, mul, add);
       if (__ballot(top > m + kSlack)) {
         const float now = fmaxf(m, top), shrink = exp2_fast(m - now);
         m = now;
@@ -716,7 +717,18 @@ __global__ __launch_bounds__(NW * 64, 2) void k_paged_many(PagedArgs a) {
         for (int d = 0; d < kDt; ++d) o[d] *= shrink;
       }
       clean((at + 1) * kPage, length_of(id1));
-      const float less = add - m;
+      // a weight is 2^(s mul + less) in one operation, whose product is not
+      // rounded as the one in m was: far from 0 the two differ by more than an
+      // exponential takes, and the scores are rounded like m first
+      float less = add - m;
+      if (__ballot(fabsf(m) > kFar)) {
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[kt][e] = __builtin_fmaf(s[kt][e], mul, add) - m;
+        mul = 1.f;
+        less = 0.f;
+      }
       v4u p[4], f[kAhead];
       float sum[2] = {0.f, 0.f};
       // pairs of weights that go beside product j of n
