@@ -39,7 +39,9 @@ using namespace svdq_dev;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNothing = -1e30f;    // the running maximum before the first key
+// The running maximum before the first key: the least finite value, so that no
+// finite score lies below it.
+constexpr float kNothing = -3.402823466e38f;
 constexpr int kCUs = 256;
 
 struct PagedArgs {

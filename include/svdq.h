@@ -552,8 +552,9 @@ SVDQ_API int svdq_gemm_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq
  * the pages hold.  Pages' places past a sequence's length may hold anything;
  * a NaN at a key that only causal masking hides can reach a query that sees
  * others.  The codes are taken exactly; P is rounded to 16 bits for the matrix
- * core; softmax statistics and sums are fp32.  o overlaps no operand.
- * 2^-80 <= scale < 2^80.
+ * core; softmax statistics and sums are fp32.  Scores may have any size that
+ * fp32 holds (times log2 e); one past it is an infinity, and below it counts as
+ * hidden.  o overlaps no operand.  2^-80 <= scale < 2^80.
  * workspace (dev, 16-byte aligned): with the bytes that
  * svdq_attention_paged_workspace_size names, calls with few queries a sequence
  * cut the keys into equal shares, which a second kernel joins in a fixed

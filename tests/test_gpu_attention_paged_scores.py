@@ -61,3 +61,11 @@ def test_one_key_outweighs_all(case, dtype, far):
         check(case, dtype, -1, power, far)
         check(case, dtype, 1, power, far)
     check(case, dtype, 1, 120, far)
+
+
+@pytest.mark.parametrize("case", CASES)
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("far", [False, True])
+def test_scores_far_below_zero(case, dtype, far):
+    for power in (98, 99, 100, 110, 120, 125):      # 2 s log2 e from -2^99.6 to -2^127
+        check(case, dtype, -1, power, far)
