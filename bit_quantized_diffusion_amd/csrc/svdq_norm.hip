@@ -13,6 +13,7 @@
 // join their sums in LDS.
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "svdq_device.h"
@@ -192,12 +193,15 @@ int launch(const NormArgs& a, hipStream_t stream) {
 //   h = x [+ residual],  y = h rstd [* w],  rstd = 1 / sqrt(mean(h^2) + eps)
 //
 // h is held in fp32 between the sum, the norm and its own store (rounded
-// once).  y is rounded to 16 bits, or (FP8) to e4m3 codes with a scale for each
-// 128 values of the row: s = max(amax, 2^-100) / 448, code = e4m3(y * (1 / s)).
-// A block of 128 is 16 consecutive lanes, so its largest magnitude is four
-// exchanges.  A NaN stays one; an infinity makes its block's scale infinite
-// and its codes 0 and NaN.  Memory-bound like the layer norm above: 4608 x 4096
-// with a residual to codes 24.1 us by itself, 5.5 TB/s.
+// once).  Its squares leave fp32's range for rows past 2^64 / sqrt(K) and, where
+// eps is too small to hide that, for very small ones, while 16 bits hold 2^-133
+// to 2^128: such rows are summed again at another scale.  y is rounded to 16
+// bits, or (FP8) to e4m3 codes with a scale for each 128 values of the row:
+// s = max(amax, 2^-100) / 448, code = e4m3(y * (1 / s)).  A block of 128 is 16
+// consecutive lanes, so its largest magnitude is four exchanges.  A NaN stays
+// one; an infinity makes its block's scale infinite and its codes 0 and NaN.
+// Memory-bound like the layer norm above: 4608 x 4096 with a residual to codes
+// 26.1 us among other calls, 5.1 TB/s.
 // ---------------------------------------------------------------------------
 
 struct RmsArgs {
@@ -233,7 +237,7 @@ __global__ __launch_bounds__(WAVES > 1 ? WAVES * 64 : 256) void k_rms_norm(RmsAr
   static_assert(!FP8 || (LANES >= 16 && !TAIL), "a block's lanes stand beside each other");
   constexpr int kThreads = WAVES * LANES;                  // threads of a row
   constexpr int kRows = WAVES > 1 ? 1 : 256 / LANES;       // rows of a workgroup
-  __shared__ float sums[WAVES];
+  __shared__ float sums[2][WAVES];
   const int t = threadIdx.x % kThreads;
   const int64_t row = (static_cast<int64_t>(blockIdx.y) * kGridX + blockIdx.x) * kRows + threadIdx.x / kThreads;
   if (row >= a.M) return;   // whole rows' lanes leave together
@@ -261,7 +265,25 @@ __global__ __launch_bounds__(WAVES > 1 ? WAVES * 64 : 256) void k_rms_norm(RmsAr
 #pragma unroll
     for (int e = 0; e < 8; ++e) square += f[c][e] * f[c][e];
   }
-  const float rstd = 1.f / sqrtf(row_total<LANES, WAVES>(square, sums) * (1.f / a.K) + a.eps);
+  const float inv_k = 1.f / a.K;
+  float total = row_total<LANES, WAVES>(square, sums[0]);
+  float rstd, lift = 1.f;
+  const bool large = total == INFINITY, small = total < 0x1p-60f && a.eps < 0x1p-60f;
+  if (large || small) {
+    // the squares leave fp32's range: those of h times a power of two, which
+    // goes into the root's reciprocal or, where that would overflow, into h
+    const float by = large ? 0x1p-80f : 0x1p90f;
+    square = 0.f;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) square += (f[c][e] * by) * (f[c][e] * by);
+    total = row_total<LANES, WAVES>(square, sums[1]);
+    rstd = (large ? by : 1.f) / sqrtf(total * inv_k + a.eps * by * by);
+    lift = large ? 1.f : by;
+  } else {
+    rstd = 1.f / sqrtf(total * inv_k + a.eps);
+  }
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
     const int k = (c * kThreads + t) * 8;
@@ -273,6 +295,9 @@ __global__ __launch_bounds__(WAVES > 1 ? WAVES * 64 : 256) void k_rms_norm(RmsAr
       else
         store8(p, pack8<E>(f[c]), a.K - k);
     }
+    if (lift != 1.f)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[c][e] *= lift;
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[c][e] *= rstd;
     if (a.weight) {

@@ -460,8 +460,8 @@ SVDQ_API int svdq_layer_norm(const void* x, int64_t ldx, const void* weight, con
  *   yq, ys    (dev) codes and scales of y, out, or both NULL; taken from the
  *             fp32 y (rounded once)
  * Either y or yq and ys is given.  y is taken from h in fp32, not from its
- * rounding.  The mean of squares is an fp32 sum: rows past about 2^60 in
- * magnitude overflow it.  sum and y do not overlap.
+ * rounding, at any size that fp32 holds: where the squares' sum leaves its
+ * range it is taken at another scale.  sum and y do not overlap.
  * 1 <= M <= 2^31 - 2^16; K from 1 to 65536, K % 16 == 0 for codes; eps >= 0
  * and finite.  16-bit pointers need 2-byte alignment only. */
 SVDQ_API int svdq_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
