@@ -119,6 +119,6 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, out=None, resi
 
     x and residual [M][K], weight [K].  Rows may be strided.  Returns y, or
     with a residual (y, h): h is the sum, rounded once (y is taken from the
-    unrounded one).  `out` may be x or residual, and so may `residual_out`,
-    but not both the same.  No gradient."""
+    unrounded one).  `out` may be x or residual, and so may `residual_out`;
+    the two share no memory (ValueError).  No gradient."""
     return _block_ops.rms_norm(x, weight, residual, eps, out, residual_out, False)

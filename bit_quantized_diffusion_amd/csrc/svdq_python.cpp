@@ -514,6 +514,30 @@ void* pointer_of(PyObject* o) {
   return ptr ? PyLong_AsVoidPtr(ptr.get()) : nullptr;
 }
 
+// Whether two matrices of 16-bit values, [rows][width] of at least 1 x 1 with
+// row strides of `width` or more, share a value.
+bool overlap(const Tensor& a, const Tensor& b) {
+  const int64_t rows = a.shape[0], width = 2 * a.shape[1], la = 2 * a.ld(), lb = 2 * b.ld();   // bytes
+  uintptr_t pa = reinterpret_cast<uintptr_t>(a.ptr), pb = reinterpret_cast<uintptr_t>(b.ptr);
+  const uintptr_t end_a = pa + (rows - 1) * la + width, end_b = pb + (rows - 1) * lb + width;
+  if (pa >= end_b || pb >= end_a) return false;
+  if (la == lb) {
+    // rows i of a and j of b meet if |pb - pa + (j - i) la| < width: the two j - i next to -(pb - pa) / la
+    const uint64_t gap = pa < pb ? pb - pa : pa - pb, steps = gap / la, rest = gap % la;
+    return (rest < static_cast<uint64_t>(width) && steps < static_cast<uint64_t>(rows)) ||
+           (static_cast<uint64_t>(la) - rest < static_cast<uint64_t>(width) && steps + 1 < static_cast<uint64_t>(rows));
+  }
+  for (int64_t i = 0, j = 0; i < rows && j < rows;) {   // both in order
+    const uintptr_t x = pa + i * la, y = pb + j * lb;
+    if (x < y + width && y < x + width) return true;
+    if (x < y)
+      ++i;
+    else
+      ++j;
+  }
+  return false;
+}
+
 // rms_norm(x, weight, residual, eps, out, residual_out, codes) -> y or (codes, scales), and h with a residual
 PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (!count_of("rms_norm", n, 7)) return nullptr;
@@ -557,6 +581,10 @@ PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
       h.reset(output(Py_None, args[0], x, 2, M, K, 0, sum));
       if (!h) return nullptr;
     }
+  }
+  if (M && K && args[4] != Py_None && args[5] != Py_None && y.ld() >= K && sum.ld() >= K && overlap(y, sum)) {
+    PyErr_SetString(PyExc_ValueError, "residual_out: shares memory with out");
+    return nullptr;
   }
   if (M && !run(x.device, [&](void* stream) {
         return svdq_rms_norm(x.ptr, x.ld(), residual.ptr, residual.ptr ? residual.ld() : 0, weight.ptr, sum.ptr,
