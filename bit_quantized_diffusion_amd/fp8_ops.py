@@ -89,14 +89,22 @@ class KVCache:
 
     def read(self, block_table_row, length: int):
         """(keys, values) of one sequence as fp32 [length][heads][head_dim], in
-        plain torch operations: for inspection and tests."""
-        ids = block_table_row[:-(-length // PAGE)].long()
-        _, heads, _, d = self.k.shape
-        scale = torch.exp2(self.exponents[ids].double()).float()
+        plain torch operations: for inspection and tests.  As the attention
+        sees them: exponents are cut to [-40, 40], and positions whose entry
+        names no page, or past the row's end, hold zeros."""
+        pages, heads, _, d = self.k.shape
+        row = block_table_row.to(device=self.k.device, dtype=torch.long)
+        ids = torch.full((-(-length // PAGE),), -1, dtype=torch.long, device=self.k.device)
+        ids[:row.numel()] = row[:ids.numel()]
+        there = (ids >= 0) & (ids < pages)
+        ids = torch.where(there, ids, 0)
+        scale = torch.exp2(self.exponents[ids].clamp(-40, 40).double()).float()
         k = self.k.view(torch.uint8)[ids].view(self.k.dtype).float() * scale[:, :, 0, None, None]
         v = self.v.view(torch.uint8)[ids].view(self.v.dtype).float() * scale[:, :, 1, None, None, None]
-        v = v.view(-1, heads, 4, d, 4, 4).permute(0, 4, 2, 5, 1, 3).reshape(-1, heads, d)
-        return k.transpose(1, 2).reshape(-1, heads, d)[:length], v[:length]
+        v = v.view(ids.numel(), heads, 4, d, 4, 4).permute(0, 1, 4, 2, 5, 3).reshape(k.shape)
+        k, v = (torch.where(there[:, None, None, None], t, 0.0).transpose(1, 2).reshape(ids.numel() * PAGE, heads, d)[:length]
+                for t in (k, v))
+        return k, v
 
 
 def rope_table(positions: int, rotary: int, base: float = 10000.0, device="cuda"):
