@@ -21,8 +21,10 @@
 //
 // Measured, 32 / 8 heads of 128, bf16: one token of each of 8 caches (up to
 // 16384 tokens, 120 MB) 31 us, of 64 caches (540 MB) 98, 5.5 TB/s: bound by
-// reading the cache.  Chunks of 2048 tokens 257 us, 970 TFLOP/s: bound by the
-// matrix core and the exponentials.
+// reading the cache.  Chunks of 2048 tokens 256 us, 970 TFLOP/s: bound by the
+// matrix core, the exponentials and the widening; the two kernels of most
+// registers (heads past 64: many rows, and tiles of 32 few rows) also reload 68
+// and 60 bytes a lane from scratch in their loops over pages.
 
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -531,7 +533,9 @@ __global__ __launch_bounds__(256) void k_paged_join(PagedArgs a) {
 //
 // K's rows in LDS are 128 DC bytes, 16-byte chunk c of row r at
 // c ^ (r % (8 DC)); V lies as the lanes read it: 16 bytes for each of 16 keys,
-// 32 dimensions and lane.
+// 32 dimensions and lane.  A thread widens half of such 16 bytes at a time: its
+// 8-byte writes at a stride of 16 use half of the banks (17 % of the LDS
+// cycles of a chunk are conflicts).
 // ---------------------------------------------------------------------------
 
 template <typename E, int DC, int NW>
@@ -832,10 +836,18 @@ struct Plan {
 };
 // Up to 32 rows a sequence a tile has them all.  With more, tiles of many rows
 // read a page once for all of them, but a tile's pages are one workgroup's:
-// few such tiles leave most CUs idle (64 tokens of 32 / 8 heads against 8000
-// keys 231 us), and equal shares of tiles of 32 rows are cheaper.  Estimated in
-// us for a table's width of keys: a page takes a tile of many rows 1.9 with one
-// workgroup a CU, 2.2 with all of them at work, and a share of 32 rows 0.6.
+// few such tiles leave most CUs idle, and equal shares of tiles of 32 rows are
+// cheaper, though each tile reads the cache for itself.  Measured on both sides
+// in us, tokens of 32 / 8 heads of 128 against 8000 keys:
+//   tokens       8   64  128  256  512  768  1024  1536
+//   shares      35   58   80  128  114  299   229     -
+//   many rows  132  244  242  240  239  239   238   238
+// The choice goes by an estimate for the table's width of keys: a page takes a
+// tile of many rows 1.9 with one workgroup a CU, 2.2 with all of them at work,
+// and a share of 32 rows 0.6.  The last is low: shares of whole tiles (512 and
+// 1024 tokens) take 1.3 times the estimate, shares that cut the tiles up to 2.5
+// times.  Of the sizes above the choice still is the faster side's but for 768
+// tokens, which take shares.
 Plan plan_for(int total, int batch, int width, int heads_q, int heads_k, int D) {
   const int64_t rows = static_cast<int64_t>(total) * (heads_q / heads_k);
   const int many = D > 64 ? 256 : 128;

@@ -15,9 +15,11 @@
 // token's query heads each.
 //
 // Measured: a token of each of 64 sequences, 32 / 8 heads of 128, 8.2 us a
-// call, the host's time for it (one that loads all it can at once takes as
-// long, and prompts 4 % longer); prompts of 141 MB in all 28.8 us by itself,
-// 4.9 TB/s, the rate of a copy.
+// call, the host's time for it, and 8.6 in a HIP graph of such calls: a chain of
+// loads (starts and lengths, the table, the rows, the exponents, the values'
+// words) that each wait for the one before.  Loading ahead costs prompts 4 %; what
+// it gives a token inside a graph was not measured.  Prompts of 141 MB in all
+// 28.8 us by itself, 4.9 TB/s, the rate of a copy.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

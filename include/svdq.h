@@ -357,7 +357,9 @@ SVDQ_API int svdq_unfused_linear_noalloc(const void* x, int M, int K,
  * o overlaps none of q, k and v.
  * head_dim: a multiple of 8, 8 to 128.  total_q, total_k >= 0; total_k and
  * rows = total_q (heads_q / heads_k) at most 2^31 - 2^16, and
- * (rows / 32 + batch) heads_k below 2^24.  0 < scale < 2^127.
+ * (rows / 32 + batch) heads_k below 2^24.  0 < scale < 2^127.  Scores lie
+ * within 2^26 of 0: past that their maximum is rounded by more than the 16
+ * bits of a weight hold.
  * workspace (dev, 16-byte aligned): with the bytes that
  * svdq_attention_workspace_size names, calls with few queries (single
  * tokens against long caches) cut the keys into parts whose results a second
@@ -485,10 +487,11 @@ SVDQ_API int svdq_pack_fp8(const uint16_t* w, int K, int N, int dtype, uint8_t* 
  *
  * xq, xs, wq, ws (dev) as above, xs and ws 4-byte aligned; bias, gate,
  * residual, y, activation and dtype (theirs) as for svdq_linear16.  Sums are
- * fp32, the blocks' in a fixed order, but that the matrix core takes the 8-bit
- * products of 8 consecutive k to the largest one's exponent E and cuts what
- * lies below 2^(E - 13) (about 1e-4 of a result of 4096 products); y is
- * rounded once and overlaps no operand but residual.
+ * fp32, the blocks' in a fixed order (a block's two scales are multiplied
+ * first: their product has to lie in fp32's range), but that the matrix core
+ * takes the 8-bit products of 8 consecutive k to the largest one's exponent E
+ * and cuts what lies below 2^(E - 13) (about 1e-4 of a result of 4096
+ * products); y is rounded once and overlaps no operand but residual.
  * M, N >= 1, M at most 2^31 - 2^16, N at most 2^28 - 32, fewer than 2^23 tiles
  * of 64 x 64 in the result; K a multiple of 16 to 2^22.
  * Results are deterministic. */
