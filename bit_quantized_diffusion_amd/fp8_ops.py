@@ -93,6 +93,7 @@ class KVCache:
         sees them: exponents are cut to [-40, 40], and positions whose entry
         names no page, or past the row's end, hold zeros."""
         pages, heads, _, d = self.k.shape
+        length = int(length)
         row = block_table_row.to(device=self.k.device, dtype=torch.long)
         ids = torch.full((-(-length // PAGE),), -1, dtype=torch.long, device=self.k.device)
         ids[:row.numel()] = row[:ids.numel()]

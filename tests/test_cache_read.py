@@ -56,3 +56,10 @@ def test_lengths():
     same(cache(), [2, 0, 3], 0)
     same(cache(), [2], 100)          # past the table
     same(cache(), [], 0)
+
+
+def test_length_from_a_tensor():
+    c, row = cache(), torch.tensor([2, 0, 3], dtype=torch.int32)
+    for length in (torch.tensor([70], dtype=torch.int32)[0], torch.tensor(70)):
+        for a, b in zip(c.read(row, length), c.read(row, 70)):
+            assert torch.equal(a, b)
